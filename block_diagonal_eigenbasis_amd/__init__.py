@@ -13,3 +13,6 @@ from ._abi import (DOBB_BF16, DOBB_F32, DOBB_NORM_COL_L2, DOBB_NORM_IDENTITY, DO
                    dobb_step, dobb_step_grouped, dobb_step_noalloc, dobb_workspace_size, lib, make_hparams,
                    status_string, DOBB_ERR_WORKSPACE, DOBB_NOALLOC_SCRATCH_BYTES, DOBB_WS_BF16_BASIS,
                    DOBB_OP_STEP_G, dobb_step_g, dobb_step_g_grouped, DOBB_REFRESH_ORTH_ITER_CHOLQR)
+from ._ops import (MX4_TILE, dobb_accumulate_moment_mx4, dobb_accumulate_moment_mx4_grouped,  # noqa: E402,F401
+                   dobb_clip_grad_norm_grouped, dobb_clip_grads_grouped, dobb_grad_norm_grouped,
+                   dobb_moment_mx4_workspace_size, dobb_mx4_dequantize, dobb_mx4_quantize, mx4_tiles)

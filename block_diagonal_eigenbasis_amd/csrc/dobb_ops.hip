@@ -1,0 +1,262 @@
+// C ABI of dobb_ops.h: host-side validation and workspace sizing.  Every computation is done by the
+// kernels in k_grads.hip, k_mx4.hip and k_moment_mx4.hip.
+#include <algorithm>
+#include <new>
+#include <vector>
+
+#include "ops_internal.h"
+
+using namespace dobb;
+
+namespace {
+
+constexpr int64_t kMaxNb = 1024;
+constexpr int64_t kMaxN = (int64_t)1 << 25;       // the product's column offsets are 32-bit
+constexpr int64_t kMaxTokens = (int64_t)1 << 40;
+
+bool dtype_ok(dobb_dtype d) { return d == DOBB_F32 || d == DOBB_BF16; }
+int64_t size_of(dobb_dtype d) { return d == DOBB_BF16 ? 2 : 4; }
+inline size_t al256(size_t x) { return (x + 255) / 256 * 256; }
+dobb_status hip_status(hipError_t e) { return e == hipSuccess ? DOBB_OK : DOBB_ERR_HIP; }
+
+dobb_status check_ws(void *ws, size_t ws_bytes, size_t need) {
+    if (need == 0) return DOBB_OK;
+    if (!ws || ((uintptr_t)ws & 255u) != 0 || ws_bytes < need) return DOBB_ERR_WORKSPACE;
+    return DOBB_OK;
+}
+
+// a list of tensors: dtypes, sizes, pointers aligned to their entries
+dobb_status check_list(int count, const int64_t *numel, const void *const *p, const dobb_dtype *dt) {
+    if (count < 1 || !numel || !p || !dt) return DOBB_ERR_INVALID_ARG;
+    for (int i = 0; i < count; ++i) {
+        if (!dtype_ok(dt[i])) return DOBB_ERR_DTYPE;
+        if (numel[i] < 0 || numel[i] > ((int64_t)1 << 44)) return DOBB_ERR_SHAPE;
+        if (numel[i] > 0 && !p[i]) return DOBB_ERR_INVALID_ARG;
+        if ((uintptr_t)p[i] & (uintptr_t)(size_of(dt[i]) - 1)) return DOBB_ERR_INVALID_ARG;
+    }
+    return DOBB_OK;
+}
+
+// Every buffer written is the tensor it is made from (same type) or apart from everything else in the
+// list: a chunk of one is then read and written by one workgroup only.
+dobb_status check_outputs(const GradArgs &a) {
+    struct Span {
+        uintptr_t lo, hi;
+        bool out;
+    };
+    std::vector<Span> v;
+    v.reserve(2 * (size_t)a.count);
+    for (int i = 0; i < a.count; ++i) {
+        if (a.numel[i] == 0) continue;
+        const uintptr_t g = (uintptr_t)a.G[i], o = (uintptr_t)a.out[i];
+        if (g != o || a.g_dtypes[i] != a.out_dtypes[i]) v.push_back({g, g + (uintptr_t)(a.numel[i] * size_of(a.g_dtypes[i])), false});
+        v.push_back({o, o + (uintptr_t)(a.numel[i] * size_of(a.out_dtypes[i])), true});
+    }
+    std::sort(v.begin(), v.end(), [](const Span &x, const Span &y) { return x.lo < y.lo; });
+    uintptr_t out_end = 0, in_end = 0;
+    for (const Span &s : v) {
+        if (s.lo < out_end || (s.out && s.lo < in_end)) return DOBB_ERR_INVALID_ARG;
+        uintptr_t &end = s.out ? out_end : in_end;
+        if (s.hi > end) end = s.hi;
+    }
+    return DOBB_OK;
+}
+
+dobb_status check_clip(const GradArgs &a, const float *total, float max_norm) {
+    dobb_status st = check_list(a.count, a.numel, a.G, a.g_dtypes);
+    if (st != DOBB_OK) return st;
+    st = check_list(a.count, a.numel, (const void *const *)a.out, a.out_dtypes);
+    if (st != DOBB_OK) return st;
+    if (!total || !(max_norm >= 0.f)) return DOBB_ERR_INVALID_ARG;
+    return check_outputs(a);
+}
+
+size_t norm_ws(int count, const int64_t *numel, const dobb_dtype *dt) {
+    return al256((size_t)grad_norm_chunks(count, numel, dt) * 8 + 8);
+}
+
+dobb_status check_capture(int64_t N, int64_t n, const void *p, dobb_dtype dt, int64_t ld, const void *codes, const void *scales) {
+    if (!p || !codes || !scales) return DOBB_ERR_INVALID_ARG;
+    if (!dtype_ok(dt)) return DOBB_ERR_DTYPE;
+    if (N < 1) return DOBB_ERR_INVALID_ARG;
+    if (N > kMaxTokens || n < 1 || n > kMaxN || ld < n) return DOBB_ERR_SHAPE;
+    if ((N / kMx4Tile + 1) * ((n + 127) / 128) > 0x7fffffff) return DOBB_ERR_SHAPE;
+    if (((uintptr_t)codes & 15u) || ((uintptr_t)scales & 3u) || ((uintptr_t)p & (uintptr_t)(size_of(dt) - 1)))
+        return DOBB_ERR_INVALID_ARG;
+    return DOBB_OK;
+}
+
+dobb_status check_moment_shape(const dobb_shape &s) {
+    if (s.n < 1 || s.n > kMaxN || s.nb < 1 || s.nb > kMaxNb || s.n % s.nb != 0) return DOBB_ERR_SHAPE;
+    return DOBB_OK;
+}
+
+// matrices of one launch: the workgroups of one split have to fit a grid
+int moment_chunk(const dobb_shape &s) {
+    const int64_t nt = (s.nb + 127) / 128;
+    const int64_t per = (s.n / s.nb) * std::max(nt * (nt + 1) / 2, (s.nb * s.nb + 255) / 256);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxMats, 0x3fffffff / per));
+}
+
+// indices of the shapes equal to shapes[i] (n and nb), if i is the first of them; empty otherwise
+std::vector<int> same_moment(int count, const dobb_shape *shapes, int i) {
+    std::vector<int> g;
+    for (int k = 0; k < count; ++k)
+        if (shapes[k].n == shapes[i].n && shapes[k].nb == shapes[i].nb) {
+            if (k < i) return {};
+            g.push_back(k);
+        }
+    return g;
+}
+
+size_t moment_ws(int count, const dobb_shape *shapes, int64_t tiles) {
+    size_t need = 0;
+    for (int i = 0; i < count; ++i) {
+        const size_t cnt = same_moment(count, shapes, i).size();
+        if (!cnt) continue;
+        const size_t chunk = (size_t)moment_chunk(shapes[i]);
+        // every launch of the group, the last one smaller: fewer matrices may take more splits
+        for (size_t c0 = 0; c0 < cnt; c0 += chunk)
+            need = std::max(need, al256(moment_mx4_ws(shapes[i].n, shapes[i].nb, (int)std::min(chunk, cnt - c0), tiles)));
+    }
+    return need;
+}
+
+dobb_status moment_grouped(int count, const dobb_shape *shapes, const void *const *codes, const void *const *scales,
+                           int64_t tiles, int64_t N, float beta, float *const *A, void *ws, size_t ws_bytes,
+                           hipStream_t stream) {
+    if (count < 1 || !shapes || !codes || !scales || !A) return DOBB_ERR_INVALID_ARG;
+    if (tiles < 1 || N < 1 || N / kMx4Tile + (N % kMx4Tile != 0) > tiles || !(beta >= 0.f && beta < 1.f)) return DOBB_ERR_INVALID_ARG;
+    if (tiles > kMaxTokens / kMx4Tile) return DOBB_ERR_SHAPE;
+    for (int i = 0; i < count; ++i) {
+        const dobb_status st = check_moment_shape(shapes[i]);
+        if (st != DOBB_OK) return st;
+        if (!codes[i] || !scales[i] || !A[i] || ((uintptr_t)codes[i] & 15u) || ((uintptr_t)scales[i] & 3u) || ((uintptr_t)A[i] & 3u))
+            return DOBB_ERR_INVALID_ARG;
+    }
+    const dobb_status st = check_ws(ws, ws_bytes, moment_ws(count, shapes, tiles));
+    if (st != DOBB_OK) return st;
+    for (int i = 0; i < count; ++i) {
+        const std::vector<int> g = same_moment(count, shapes, i);
+        const size_t chunk = (size_t)moment_chunk(shapes[i]);
+        for (size_t c0 = 0; c0 < g.size(); c0 += chunk) {
+            const void *cs[kMaxMats], *ss[kMaxMats];
+            float *as[kMaxMats];
+            MomentMx4Args a{};
+            a.count = (int)std::min(chunk, g.size() - c0);
+            for (int k = 0; k < a.count; ++k) { cs[k] = codes[g[c0 + k]]; ss[k] = scales[g[c0 + k]]; as[k] = A[g[c0 + k]]; }
+            a.n = shapes[i].n;
+            a.nb = shapes[i].nb;
+            a.tiles = tiles;
+            a.N = N;
+            a.codes = cs;
+            a.scales = ss;
+            a.A = as;
+            a.beta = beta;
+            a.nsplit = moment_mx4_splits(a.n, a.nb, a.count, tiles);
+            a.partial = (float *)ws;
+            const dobb_status r = hip_status(launch_moment_mx4(a, stream));
+            if (r != DOBB_OK) return r;
+        }
+    }
+    return DOBB_OK;
+}
+
+// nothing thrown inside (host memory for the lists) leaves a C entry
+template <typename F>
+dobb_status guarded(F f) {
+    try {
+        return f();
+    } catch (...) {
+        return DOBB_ERR_INVALID_ARG;
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dobb_grad_norm_workspace_size(int count, const int64_t *numel, const dobb_dtype *g_dtypes) {
+    if (count < 1 || !numel || !g_dtypes) return 0;
+    for (int i = 0; i < count; ++i)
+        if (!dtype_ok(g_dtypes[i]) || numel[i] < 0 || numel[i] > ((int64_t)1 << 44)) return 0;
+    return norm_ws(count, numel, g_dtypes);
+}
+
+dobb_status dobb_grad_norm_grouped(int count, const int64_t *numel, const void *const *G, const dobb_dtype *g_dtypes,
+                                   float *norms, float *total, void *ws, size_t ws_bytes, dobb_stream_t stream) {
+    dobb_status st = check_list(count, numel, G, g_dtypes);
+    if (st != DOBB_OK) return st;
+    if (!total) return DOBB_ERR_INVALID_ARG;
+    st = check_ws(ws, ws_bytes, norm_ws(count, numel, g_dtypes));
+    if (st != DOBB_OK) return st;
+    const GradArgs a{count, numel, G, g_dtypes, nullptr, nullptr};
+    return hip_status(launch_grad_norm(a, norms, total, (double *)ws, (hipStream_t)stream));
+}
+
+dobb_status dobb_clip_grads_grouped(int count, const int64_t *numel, const void *const *G, const dobb_dtype *g_dtypes,
+                                    void *const *out, const dobb_dtype *out_dtypes, const float *total, float max_norm,
+                                    dobb_stream_t stream) {
+    return guarded([&]() -> dobb_status {
+        const GradArgs a{count, numel, G, g_dtypes, out, out_dtypes};
+        const dobb_status st = check_clip(a, total, max_norm);
+        if (st != DOBB_OK) return st;
+        return hip_status(launch_grad_clip(a, total, max_norm, (hipStream_t)stream));
+    });
+}
+
+dobb_status dobb_clip_grad_norm_grouped(int count, const int64_t *numel, const void *const *G, const dobb_dtype *g_dtypes,
+                                        void *const *out, const dobb_dtype *out_dtypes, float max_norm, float *norms,
+                                        float *total, void *ws, size_t ws_bytes, dobb_stream_t stream) {
+    return guarded([&]() -> dobb_status {
+        const GradArgs a{count, numel, G, g_dtypes, out, out_dtypes};
+        dobb_status st = check_clip(a, total, max_norm);
+        if (st != DOBB_OK) return st;
+        st = check_ws(ws, ws_bytes, norm_ws(count, numel, g_dtypes));
+        if (st != DOBB_OK) return st;
+        st = hip_status(launch_grad_norm(a, norms, total, (double *)ws, (hipStream_t)stream));
+        if (st != DOBB_OK) return st;
+        return hip_status(launch_grad_clip(a, total, max_norm, (hipStream_t)stream));
+    });
+}
+
+dobb_status dobb_mx4_quantize(int64_t N, int64_t n, const void *X, dobb_dtype x_dtype, int64_t ldx, void *codes, void *scales,
+                              dobb_stream_t stream) {
+    const dobb_status st = check_capture(N, n, X, x_dtype, ldx, codes, scales);
+    if (st != DOBB_OK) return st;
+    return hip_status(launch_mx4_quantize(N, n, X, x_dtype == DOBB_BF16, ldx, codes, scales, (hipStream_t)stream));
+}
+
+dobb_status dobb_mx4_dequantize(int64_t N, int64_t n, const void *codes, const void *scales, void *out, dobb_dtype out_dtype,
+                                int64_t ldo, dobb_stream_t stream) {
+    const dobb_status st = check_capture(N, n, out, out_dtype, ldo, codes, scales);
+    if (st != DOBB_OK) return st;
+    return hip_status(launch_mx4_dequantize(N, n, codes, scales, out, out_dtype == DOBB_BF16, ldo, (hipStream_t)stream));
+}
+
+size_t dobb_moment_mx4_workspace_size(int count, const dobb_shape *shapes, int64_t tiles) {
+    if (count < 1 || !shapes || tiles < 1 || tiles > kMaxTokens / kMx4Tile) return 0;
+    for (int i = 0; i < count; ++i)
+        if (check_moment_shape(shapes[i]) != DOBB_OK) return 0;
+    try {
+        return moment_ws(count, shapes, tiles);
+    } catch (...) {
+        return 0;
+    }
+}
+
+dobb_status dobb_accumulate_moment_mx4_grouped(int count, const dobb_shape *shapes, const void *const *codes,
+                                               const void *const *scales, int64_t tiles, int64_t N, float beta,
+                                               float *const *A, void *ws, size_t ws_bytes, dobb_stream_t stream) {
+    return guarded([&]() -> dobb_status {
+        return moment_grouped(count, shapes, codes, scales, tiles, N, beta, A, ws, ws_bytes, (hipStream_t)stream);
+    });
+}
+
+dobb_status dobb_accumulate_moment_mx4(const dobb_shape *s, const void *codes, const void *scales, int64_t tiles, int64_t N,
+                                       float beta, float *A, void *ws, size_t ws_bytes, dobb_stream_t stream) {
+    if (!s) return DOBB_ERR_INVALID_ARG;
+    return dobb_accumulate_moment_mx4_grouped(1, s, &codes, &scales, tiles, N, beta, &A, ws, ws_bytes, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,174 @@
+// Captures in MXFP4 (OCP Microscaling Formats: e2m1 elements, one e8m0 scale per 32 tokens of a
+// column): quantising and reading back.  Layout: dobb_ops.h.
+//
+// One wave takes one group (32 tokens) of 128 columns, two neighbouring columns a lane: 32 row reads of
+// 256 (bf16) or 512 (fp32) contiguous bytes, all in flight, no exchange between lanes for the largest
+// magnitude, and 32 contiguous bytes of codes a lane.  The four waves of a workgroup take the four
+// groups of a tile, whose scale bytes leave together through LDS.  Both directions are bound by HBM.
+// The conversions are gfx950's scaled ones (v_cvt_scalef32_pk_fp4_f32 and back): nearest, ties to even,
+// saturating at 6, exact for every scale from 2^-127 (checked against the definition on the card).
+#include "ops_internal.h"
+
+namespace dobb {
+namespace {
+
+constexpr int kCols = 128;   // columns per workgroup
+
+template <bool BF16>
+struct __attribute__((packed, aligned(2))) Pair { uint32_t w[BF16 ? 1 : 2]; };
+
+// the largest magnitude's bits, as fp32: its exponent field is bits >> 23, from 255 on not finite
+__device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+template <bool BF16>
+__global__ void __launch_bounds__(256) k_mx4_quantize(int64_t N, int64_t n, int64_t ldx, int64_t colblocks, const void *X,
+                                                      uint4 *codes, uint32_t *scales) {
+    __shared__ uint8_t sc[kCols][4];
+    const int64_t tile = blockIdx.x / colblocks;
+    const int64_t c0 = (blockIdx.x % colblocks) * kCols;
+    const int g = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t c = c0 + 2 * lane;
+    const int64_t t0 = tile * kMx4Tile + 32 * g;
+    const int rows = N - t0 < 0 ? 0 : N - t0 < 32 ? (int)(N - t0) : 32;
+    constexpr int ES = BF16 ? 2 : 4;
+    const char *x = (const char *)X + ((t0 < N ? t0 : 0) * ldx + c) * ES;
+    float a[32], b[32];
+    if (c + 1 < n && rows == 32) {
+        Pair<BF16> v[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = *(const Pair<BF16> *)(x + k * ldx * ES);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+            a[k] = BF16 ? __uint_as_float(v[k].w[0] << 16) : __uint_as_float(v[k].w[0]);
+            b[k] = BF16 ? __uint_as_float(v[k].w[0] & 0xffff0000u) : __uint_as_float(v[k].w[BF16 ? 0 : 1]);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+            const bool in = k < rows;
+            const char *r = x + k * ldx * ES;
+            a[k] = in && c < n ? (BF16 ? bf16_to_f32(*(const uint16_t *)r) : *(const float *)r) : 0.f;
+            b[k] = in && c + 1 < n ? (BF16 ? bf16_to_f32(*(const uint16_t *)(r + ES)) : *(const float *)(r + ES)) : 0.f;
+        }
+    }
+    uint32_t ma = 0, mb = 0;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+        ma = max(ma, mag(a[k]));
+        mb = max(mb, mag(b[k]));
+    }
+    uint32_t ea = ma >> 23, eb = mb >> 23;                     // exponent + 127; the scale is two below it
+    const bool na = ea == 255, nb = eb == 255;
+    ea = ea < 2 ? 0 : ea - 2;
+    eb = eb < 2 ? 0 : eb - 2;
+    const float sa = __uint_as_float(ea << 23), sb = __uint_as_float(eb << 23);   // 0 stands for 2^-127
+    uint32_t qa[4], qb[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        uint32_t p = 0, q = 0;
+        const int k = 8 * w;
+        p = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(p, a[k], a[k + 1], sa, 0);
+        p = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(p, a[k + 2], a[k + 3], sa, 1);
+        p = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(p, a[k + 4], a[k + 5], sa, 2);
+        p = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(p, a[k + 6], a[k + 7], sa, 3);
+        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, b[k], b[k + 1], sb, 0);
+        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, b[k + 2], b[k + 3], sb, 1);
+        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, b[k + 4], b[k + 5], sb, 2);
+        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, b[k + 6], b[k + 7], sb, 3);
+        qa[w] = na ? 0u : p;
+        qb[w] = nb ? 0u : q;
+    }
+    uint4 *o = codes + (tile * 4 + g) * n + c;
+    if (c < n) o[0] = uint4{qa[0], qa[1], qa[2], qa[3]};
+    if (c + 1 < n) o[1] = uint4{qb[0], qb[1], qb[2], qb[3]};
+    sc[2 * lane][g] = (uint8_t)(na ? 255u : ea);
+    sc[2 * lane + 1][g] = (uint8_t)(nb ? 255u : eb);
+    __syncthreads();
+    if (threadIdx.x < kCols && c0 + threadIdx.x < n) scales[tile * n + c0 + threadIdx.x] = *(const uint32_t *)sc[threadIdx.x];
+}
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+template <bool BF16>
+__global__ void __launch_bounds__(256) k_mx4_dequantize(int64_t N, int64_t n, int64_t ldo, int64_t colblocks, const uint4 *codes,
+                                                        const uint8_t *scales, void *out) {
+    const int64_t tile = blockIdx.x / colblocks;
+    const int64_t c0 = (blockIdx.x % colblocks) * kCols;
+    const int g = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t c = c0 + 2 * lane;
+    const int64_t t0 = tile * kMx4Tile + 32 * g;
+    if (c >= n || t0 >= N) return;
+    const int rows = N - t0 < 32 ? (int)(N - t0) : 32;
+    const bool two = c + 1 < n;
+    const uint4 *p = codes + (tile * 4 + g) * n + c;
+    const uint4 ca = p[0], cb = two ? p[1] : uint4{0, 0, 0, 0};
+    const uint8_t *s = scales + (tile * n + c) * 4 + g;
+    const uint32_t ea = s[0], eb = two ? s[4] : 0;
+    // the scale's float has e as its exponent field (0: 2^-127); 255 reads back as NaN
+    const float sa = __uint_as_float(ea << 23), sb = __uint_as_float(eb << 23);
+    const uint32_t wa[4] = {ca.x, ca.y, ca.z, ca.w}, wb[4] = {cb.x, cb.y, cb.z, cb.w};
+    constexpr int ES = BF16 ? 2 : 4;
+    char *o = (char *)out + (t0 * ldo + c) * ES;
+    float a[32], b[32];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        f32x2 x;
+#define DOBB_MX4_PAIR(k)                                                     \
+        x = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(wa[w], sa, k);          \
+        a[8 * w + 2 * k] = x[0]; a[8 * w + 2 * k + 1] = x[1];                \
+        x = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(wb[w], sb, k);          \
+        b[8 * w + 2 * k] = x[0]; b[8 * w + 2 * k + 1] = x[1];
+        DOBB_MX4_PAIR(0) DOBB_MX4_PAIR(1) DOBB_MX4_PAIR(2) DOBB_MX4_PAIR(3)
+#undef DOBB_MX4_PAIR
+    }
+    const float nan = __builtin_nanf("");
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+        if (ea == 255) a[k] = nan;
+        if (eb == 255) b[k] = nan;
+    }
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+        if (k >= rows) break;
+        char *r = o + k * ldo * ES;
+        if (two) {
+            Pair<BF16> v;
+            if (BF16) v.w[0] = (uint32_t)f32_to_bf16(a[k]) | ((uint32_t)f32_to_bf16(b[k]) << 16);
+            else { v.w[0] = __float_as_uint(a[k]); v.w[BF16 ? 0 : 1] = __float_as_uint(b[k]); }
+            *(Pair<BF16> *)r = v;
+        } else if (BF16) *(uint16_t *)r = f32_to_bf16(a[k]);
+        else *(float *)r = a[k];
+    }
+}
+
+// workgroups of a capture, 0 if a grid cannot hold them
+unsigned mx4_grid(int64_t N, int64_t n, int64_t *colblocks) {
+    *colblocks = (n + kCols - 1) / kCols;
+    const int64_t tiles = N / kMx4Tile + (N % kMx4Tile != 0);
+    if (tiles > 0x7fffffff / *colblocks) return 0;
+    return (unsigned)(tiles * *colblocks);
+}
+
+}  // namespace
+
+hipError_t launch_mx4_quantize(int64_t N, int64_t n, const void *X, bool bf16, int64_t ldx, void *codes, void *scales,
+                               hipStream_t s) {
+    int64_t cb;
+    const unsigned grid = mx4_grid(N, n, &cb);
+    if (!grid) return hipErrorInvalidValue;
+    if (bf16) DOBB_LAUNCH("mx4_quantize", s, k_mx4_quantize<true>, dim3(grid), dim3(256), 0, N, n, ldx, cb, X, (uint4 *)codes, (uint32_t *)scales);
+    else DOBB_LAUNCH("mx4_quantize", s, k_mx4_quantize<false>, dim3(grid), dim3(256), 0, N, n, ldx, cb, X, (uint4 *)codes, (uint32_t *)scales);
+    return hipGetLastError();
+}
+
+hipError_t launch_mx4_dequantize(int64_t N, int64_t n, const void *codes, const void *scales, void *out, bool bf16,
+                                 int64_t ldo, hipStream_t s) {
+    int64_t cb;
+    const unsigned grid = mx4_grid(N, n, &cb);
+    if (!grid) return hipErrorInvalidValue;
+    if (bf16) DOBB_LAUNCH("mx4_dequantize", s, k_mx4_dequantize<true>, dim3(grid), dim3(256), 0, N, n, ldo, cb, (const uint4 *)codes, (const uint8_t *)scales, out);
+    else DOBB_LAUNCH("mx4_dequantize", s, k_mx4_dequantize<false>, dim3(grid), dim3(256), 0, N, n, ldo, cb, (const uint4 *)codes, (const uint8_t *)scales, out);
+    return hipGetLastError();
+}
+
+}  // namespace dobb
