@@ -11,7 +11,7 @@ using namespace dobb;
 namespace {
 
 constexpr int64_t kMaxNb = 1024;
-constexpr int64_t kMaxN = (int64_t)1 << 25;       // the product's column offsets are 32-bit
+constexpr int64_t kMaxN = (int64_t)1 << 24;       // the product's column offsets are 32-bit
 constexpr int64_t kMaxTokens = (int64_t)1 << 40;
 
 bool dtype_ok(dobb_dtype d) { return d == DOBB_F32 || d == DOBB_BF16; }
@@ -91,34 +91,34 @@ dobb_status check_moment_shape(const dobb_shape &s) {
     return DOBB_OK;
 }
 
-// matrices of one launch: the workgroups of one split have to fit a grid
-int moment_chunk(const dobb_shape &s) {
-    const int64_t nt = (s.nb + 127) / 128;
-    const int64_t per = (s.n / s.nb) * std::max(nt * (nt + 1) / 2, (s.nb * s.nb + 255) / 256);
-    return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxMats, 0x3fffffff / per));
-}
+// One launch of a grouped call: matrices with blocks of one width, as many as the table and a grid hold
+struct MomentLaunch {
+    std::vector<int> idx;
+    int64_t nb, blocks;
+};
 
-// indices of the shapes equal to shapes[i] (n and nb), if i is the first of them; empty otherwise
-std::vector<int> same_moment(int count, const dobb_shape *shapes, int i) {
-    std::vector<int> g;
-    for (int k = 0; k < count; ++k)
-        if (shapes[k].n == shapes[i].n && shapes[k].nb == shapes[i].nb) {
-            if (k < i) return {};
-            g.push_back(k);
-        }
-    return g;
-}
-
-size_t moment_ws(int count, const dobb_shape *shapes, int64_t tiles) {
-    size_t need = 0;
+std::vector<MomentLaunch> moment_launches(int count, const dobb_shape *shapes) {
+    std::vector<MomentLaunch> out, open;
     for (int i = 0; i < count; ++i) {
-        const size_t cnt = same_moment(count, shapes, i).size();
-        if (!cnt) continue;
-        const size_t chunk = (size_t)moment_chunk(shapes[i]);
-        // every launch of the group, the last one smaller: fewer matrices may take more splits
-        for (size_t c0 = 0; c0 < cnt; c0 += chunk)
-            need = std::max(need, al256(moment_mx4_ws(shapes[i].n, shapes[i].nb, (int)std::min(chunk, cnt - c0), tiles)));
+        const int64_t nb = shapes[i].nb, blocks = shapes[i].n / nb;
+        const int64_t most = 0x3fffffff / std::max<int64_t>(64, (nb * nb + 255) / 256);
+        size_t k = 0;
+        while (k < open.size() && open[k].nb != nb) ++k;
+        if (k == open.size()) open.push_back({{}, nb, 0});
+        if (!open[k].idx.empty() && ((int)open[k].idx.size() == kMomentMats || open[k].blocks + blocks > most)) {
+            out.push_back(open[k]);
+            open[k] = {{}, nb, 0};
+        }
+        open[k].idx.push_back(i);
+        open[k].blocks += blocks;
     }
+    out.insert(out.end(), open.begin(), open.end());
+    return out;
+}
+
+size_t moment_ws(const std::vector<MomentLaunch> &launches, int64_t tiles) {
+    size_t need = 0;
+    for (const MomentLaunch &l : launches) need = std::max(need, al256(moment_mx4_ws(l.nb, l.blocks, tiles)));
     return need;
 }
 
@@ -134,30 +134,31 @@ dobb_status moment_grouped(int count, const dobb_shape *shapes, const void *cons
         if (!codes[i] || !scales[i] || !A[i] || ((uintptr_t)codes[i] & 15u) || ((uintptr_t)scales[i] & 3u) || ((uintptr_t)A[i] & 3u))
             return DOBB_ERR_INVALID_ARG;
     }
-    const dobb_status st = check_ws(ws, ws_bytes, moment_ws(count, shapes, tiles));
+    const std::vector<MomentLaunch> launches = moment_launches(count, shapes);
+    const dobb_status st = check_ws(ws, ws_bytes, moment_ws(launches, tiles));
     if (st != DOBB_OK) return st;
-    for (int i = 0; i < count; ++i) {
-        const std::vector<int> g = same_moment(count, shapes, i);
-        const size_t chunk = (size_t)moment_chunk(shapes[i]);
-        for (size_t c0 = 0; c0 < g.size(); c0 += chunk) {
-            const void *cs[kMaxMats], *ss[kMaxMats];
-            float *as[kMaxMats];
-            MomentMx4Args a{};
-            a.count = (int)std::min(chunk, g.size() - c0);
-            for (int k = 0; k < a.count; ++k) { cs[k] = codes[g[c0 + k]]; ss[k] = scales[g[c0 + k]]; as[k] = A[g[c0 + k]]; }
-            a.n = shapes[i].n;
-            a.nb = shapes[i].nb;
-            a.tiles = tiles;
-            a.N = N;
-            a.codes = cs;
-            a.scales = ss;
-            a.A = as;
-            a.beta = beta;
-            a.nsplit = moment_mx4_splits(a.n, a.nb, a.count, tiles);
-            a.partial = (float *)ws;
-            const dobb_status r = hip_status(launch_moment_mx4(a, stream));
-            if (r != DOBB_OK) return r;
+    for (const MomentLaunch &l : launches) {
+        const void *cs[kMomentMats], *ss[kMomentMats];
+        float *as[kMomentMats];
+        int64_t ns[kMomentMats];
+        MomentMx4Args a{};
+        a.count = (int)l.idx.size();
+        for (int k = 0; k < a.count; ++k) {
+            const int i = l.idx[k];
+            cs[k] = codes[i]; ss[k] = scales[i]; as[k] = A[i]; ns[k] = shapes[i].n;
         }
+        a.nb = l.nb;
+        a.tiles = tiles;
+        a.N = N;
+        a.n = ns;
+        a.codes = cs;
+        a.scales = ss;
+        a.A = as;
+        a.beta = beta;
+        a.nsplit = moment_mx4_splits(l.nb, l.blocks, tiles);
+        a.partial = (float *)ws;
+        const dobb_status r = hip_status(launch_moment_mx4(a, stream));
+        if (r != DOBB_OK) return r;
     }
     return DOBB_OK;
 }
@@ -239,7 +240,7 @@ size_t dobb_moment_mx4_workspace_size(int count, const dobb_shape *shapes, int64
     for (int i = 0; i < count; ++i)
         if (check_moment_shape(shapes[i]) != DOBB_OK) return 0;
     try {
-        return moment_ws(count, shapes, tiles);
+        return moment_ws(moment_launches(count, shapes), tiles);
     } catch (...) {
         return 0;
     }

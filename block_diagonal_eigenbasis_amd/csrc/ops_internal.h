@@ -25,18 +25,20 @@ hipError_t launch_mx4_quantize(int64_t N, int64_t n, const void *X, bool bf16, i
 hipError_t launch_mx4_dequantize(int64_t N, int64_t n, const void *codes, const void *scales, void *out, bool bf16,
                                  int64_t ldo, hipStream_t s);
 
+constexpr int kMomentMats = 96;       // matrices of one launch
 struct MomentMx4Args {
-    int count;                        // matrices, all of one shape; at most kMaxMats
-    int64_t n, nb, tiles, N;
+    int count;                        // matrices with blocks of one width; at most kMomentMats
+    int64_t nb, tiles, N;
+    const int64_t *n;                 // columns of each matrix
     const void *const *codes;
     const void *const *scales;
     float *const *A;
     float beta;
     int nsplit;
-    float *partial;                   // nsplit > 1: count x B x nsplit x nb x nb
+    float *partial;                   // nsplit > 1: blocks x nsplit x nb x nb
 };
-int moment_mx4_splits(int64_t n, int64_t nb, int count, int64_t tiles);
-size_t moment_mx4_ws(int64_t n, int64_t nb, int count, int64_t tiles);
+int moment_mx4_splits(int64_t nb, int64_t blocks, int64_t tiles);
+size_t moment_mx4_ws(int64_t nb, int64_t blocks, int64_t tiles);
 hipError_t launch_moment_mx4(const MomentMx4Args &a, hipStream_t s);
 
 }  // namespace dobb

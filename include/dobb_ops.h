@@ -73,8 +73,8 @@ dobb_status dobb_mx4_dequantize(int64_t N, int64_t n, const void *codes, const v
 /* dobb_accumulate_moment from a capture in MXFP4:
  *   A_b <- beta * A_b + (1 - beta) * (1/N) * sum_t x_{t,b} x_{t,b}^T   over all `tiles` tiles.
  * N is the divisor, the tokens the tiles hold (1 <= N <= 128 tiles); s->n, s->nb as for
- * dobb_accumulate_moment (n <= 2^25).  Products are formed on the matrix cores and summed in fp32 over at
- * most 4096 tokens, those sums over at most 16384 tokens in fp32 and beyond in fp64.  A (symmetric) is
+ * dobb_accumulate_moment (n <= 2^24).  Products are formed on the matrix cores and summed in fp32 over at
+ * most 16384 tokens, those sums in fp64.  A (symmetric) is
  * read when beta > 0 and the result is exactly symmetric. */
 size_t dobb_moment_mx4_workspace_size(int count, const dobb_shape *shapes, int64_t tiles); /* 0: bad arguments, or no scratch needed */
 dobb_status dobb_accumulate_moment_mx4(const dobb_shape *s, const void *codes, const void *scales, int64_t tiles,

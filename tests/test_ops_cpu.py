@@ -107,7 +107,7 @@ def test_mx4_refusals():
         assert a == b
         return a
     assert both(X=None) == INVALID and both(codes=None) == INVALID and both(scales=None) == INVALID
-    assert both(N=0) == INVALID and both(n=0) == SHAPE and both(ld=39) == SHAPE and both(n=(1 << 25) + 1, ld=1 << 26) == SHAPE
+    assert both(N=0) == INVALID and both(n=0) == SHAPE and both(ld=39) == SHAPE and both(n=(1 << 24) + 1, ld=1 << 26) == SHAPE
     assert both(dt=2) == DTYPE
     assert both(codes=FAKE + 8) == INVALID and both(scales=FAKE + 2) == INVALID and both(X=FAKE + 2) == INVALID
     assert both(N=1 << 39, n=1 << 20, ld=1 << 20) == SHAPE            # more tiles than a grid holds
@@ -134,8 +134,8 @@ def test_moment_mx4_refusals():
     # one tile has nothing to split; a long capture is split whatever the grid
     assert size([(1, 768, 192)], 1) == 0
     assert size([(1, 128 * 1024, 128)], 1024) > 0
-    # the last launch of a group of many may need more than the full ones before it
-    assert size([(1, 1600, 100)] * 49, 128) >= size([(1, 1600, 100)], 128)
+    # the last launch of a group of many (one matrix here) is split where the full one before it is not
+    assert size([(1, 1600, 100)] * 97, 128) >= size([(1, 1600, 100)], 128) > 0
 
 
 def test_python_refusals_without_a_gpu():
