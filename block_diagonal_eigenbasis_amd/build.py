@@ -1,8 +1,9 @@
-"""Build libdobb.so (HIP, gfx950) in-tree with hipcc.
+"""Build libdobb.so (HIP, gfx950) in-tree with hipcc, and the host module of the binding with g++.
 
 Every kernel source is compiled for gfx950 only, with packed-fp32 instructions disabled
 (-Xclang -target-feature -Xclang -packed-fp32-ops), and linked into one shared library next to this
-file.  build() always recompiles.
+file; _dobb_host.so (csrc/host_ops.cpp, host code against torch's headers) is linked against it.
+build() always recompiles.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ from concurrent.futures import ThreadPoolExecutor
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libdobb.so")
+HOST = os.path.join(PKG, "_dobb_host.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 SOURCES = ["dobb_api.hip", "dobb_ops.hip", "k_grads.hip", "k_mx4.hip", "k_moment_mx4.hip", "k_basis.hip", "k_cholqr.hip", "k_step.hip", "k_step_g.hip", "k_step_bf16.hip", "k_step_fused.hip", "k_accumulate.hip", "k_refresh.hip", "k_qr.hip", "k_step_rows.hip", "k_step_wide.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -30,6 +32,24 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_host() -> None:
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    inc = [x for d in cpp_extension.include_paths("cuda") for x in ("-isystem", d)]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = HOST + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-fPIC", "-shared", "-std=c++17", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc, "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "host_ops.cpp"), "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch", "-lc10", "-lc10_hip",
+           "-L", PKG, "-ldobb", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on host_ops.cpp:\n{r.stderr}")
+    os.replace(tmp, HOST)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     with ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 1)) as ex:
@@ -40,8 +60,9 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    _build_host()
     if verbose:
-        print(f"built {LIB}")
+        print(f"built {LIB} and {HOST}")
     return LIB
 
 
