@@ -3,7 +3,8 @@
 The method is "Dobb: Shard-Local Preconditioning in Block-Diagonal Eigenbases" (arXiv 2610.39412):
 per weight, block-diagonal input-activation second moments (EMA), a complete eigenbasis per block,
 and the update sign(M_b Q_b) Q_b^T.  ``_abi`` binds the C entry points one to one; ``optimizer``
-drives them with a refresh cadence, as a torch optimizer.
+drives them with a refresh cadence, as a torch optimizer.  ``_ops`` adds what a training loop runs around
+the step: gradient norms and clipping over tensor lists, and captures held in MXFP4.
 """
 from ._abi import (DOBB_BF16, DOBB_F32, DOBB_NORM_COL_L2, DOBB_NORM_IDENTITY, DOBB_NORM_SIGN,  # noqa: F401
                    DOBB_OP_ACCUMULATE, DOBB_OP_REFRESH, DOBB_OP_STEP, DOBB_REFRESH_EXACT,

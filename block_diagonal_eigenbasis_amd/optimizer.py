@@ -20,7 +20,7 @@ import math
 
 import torch
 
-from . import _abi
+from . import _abi, _ops
 
 
 def default_update_scale(m: int, n: int, tau: float = 0.2) -> float:
@@ -30,6 +30,75 @@ def default_update_scale(m: int, n: int, tau: float = 0.2) -> float:
 def default_update_scale_g(m: int, n: int, tau: float = 0.2) -> float:
     """Dobb-G (Table 9): RMS tau sqrt(max(m, n)/n) for the sign update."""
     return tau * math.sqrt(max(m, n) / n)
+
+
+class Mx4Capture:
+    """Captured activations or output gradients (tokens x n) held in MXFP4: 17/32 byte an entry instead of
+    2 or 4, from the forward (or backward) pass to the refresh that takes their second moment.  `parts` are
+    the token counts of the micro-batches it holds, each from a tile of 128 tokens of its own."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, parts):
+        self.codes, self.scales, self.parts = codes, scales, tuple(int(k) for k in parts)
+        if any(k < 1 for k in self.parts) or sum(_ops.mx4_tiles(k) for k in self.parts) != codes.shape[0]:
+            raise ValueError("the tiles of the parts do not add up to those of the codes")
+
+    @classmethod
+    def quantize(cls, x: torch.Tensor) -> "Mx4Capture":
+        """(tokens x n) fp32 or bf16 -> MXFP4 (dobb_mx4_quantize)."""
+        codes, scales = _ops.dobb_mx4_quantize(x)
+        return cls(codes, scales, (x.shape[0],))
+
+    @classmethod
+    def cat(cls, captures) -> "Mx4Capture":
+        """Captures of several micro-batches as one."""
+        captures = list(captures)
+        if len(captures) == 1:
+            return captures[0]
+        if not captures or len({c.shape[1] for c in captures}) != 1:
+            raise ValueError("captures of one width, at least one")
+        return cls(torch.cat([c.codes for c in captures]), torch.cat([c.scales for c in captures]),
+                   [k for c in captures for k in c.parts])
+
+    def dequantize(self, dtype: torch.dtype = torch.float32) -> torch.Tensor:
+        """The (tokens x n) values held (dobb_mx4_dequantize)."""
+        out = torch.empty(*self.shape, dtype=dtype, device=self.device)
+        tile = row = 0
+        for k in self.parts:
+            t = _ops.mx4_tiles(k)
+            _ops.dobb_mx4_dequantize(self.codes[tile:tile + t], self.scales[tile:tile + t], k, dtype, out=out[row:row + k])
+            tile, row = tile + t, row + k
+        return out
+
+    @property
+    def shape(self):
+        return (sum(self.parts), self.codes.shape[2])
+
+    @property
+    def tiles(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def clip_grad_norm_(parameters, max_norm: float) -> torch.Tensor:
+    """Scale the gradients of the parameters (or one parameter) in place so that their global l2 norm is at
+    most max_norm, by min(1, max_norm / (norm + 1e-6)); returns the norm before, as a device scalar.
+    Gradients are contiguous, fp32 or bf16, on one device; parameters without one are passed over, and a
+    gradient shared by several counts once.  Call it over a whole model's parameters where several
+    optimizers share them (``Dobb(max_grad_norm=...)`` clips over its own)."""
+    if isinstance(parameters, torch.Tensor):
+        parameters = [parameters]
+    grads, seen = [], set()
+    for p in parameters:
+        g = p.grad
+        if g is not None and (g.numel() == 0 or g.data_ptr() not in seen):
+            seen.add(g.data_ptr())
+            grads.append(g)
+    if not grads:
+        return torch.zeros(())
+    return _ops.dobb_clip_grad_norm_grouped(grads, max_norm)
 
 
 def _arr(ptrs):
@@ -100,7 +169,10 @@ class DobbGroup:
     caller's stream: the two kernel families then overlap (the wide blocks' refresh is a chain of
     latency-bound panel launches).  basis_dtype=torch.bfloat16 stores every Q_b in bf16.
     side="output" runs Dobb-G: block_sizes divide the output dimensions, the moments are captured from
-    output gradients (accumulate takes N x m tensors) and the step is dobb_step_g."""
+    output gradients (accumulate takes N x m tensors) and the step is dobb_step_g.
+    Captures may be tensors or ``Mx4Capture``s, mixed.  With max_grad_norm, step and refresh_step first clip
+    the gradients in place to that global norm over the set; `grad_norm` (device scalar) then holds the
+    norm before."""
 
     def __init__(self, weights, block_sizes, grads=None, n_tokens: int = 0, lr: float = 2.5e-3,
                  weight_decay: float = 0.0, momentum: float = 0.9, tau: float = 0.2, nesterov: bool = False,
@@ -145,6 +217,7 @@ class DobbGroup:
         self._parts = []
         self.set_streams(streams)
         self.refreshes = 0
+        self.grad_norm = torch.zeros((), dtype=torch.float32, device=dev)
 
     def cap_dim(self, i: int) -> int:
         """The dimension the moments of weight i are captured on: n (inputs) or m (outputs, Dobb-G)."""
@@ -196,9 +269,18 @@ class DobbGroup:
                 part.ensure(part.need(self, N))
             self.n_tokens = N
 
+    @staticmethod
+    def _dense_tokens(xs) -> int:
+        """Tokens of the longest capture given as a tensor (those in MXFP4 size their own workspace)."""
+        return max((x.shape[0] for x in xs if not isinstance(x, Mx4Capture)), default=0)
+
     def _accumulate(self, part, sh, xs, beta):
-        """One grouped capture per (activation dtype, token count) among the part's weights."""
-        for sub in _split(part.idx, lambda i: (xs[i].dtype, xs[i].shape[0])):
+        """One grouped capture per (activation dtype, token count), and per (tiles, token count) of those in
+        MXFP4, among the part's weights."""
+        for sub, shapes in self._mx4_groups(part, xs):
+            self._accumulate_mx4(part, sh, sub, shapes, xs, beta)
+        dense = [i for i in part.idx if not isinstance(xs[i], Mx4Capture)]
+        for sub in _split(dense, lambda i: (xs[i].dtype, xs[i].shape[0])):
             if len(sub) == part.count:
                 ash, A, ldx = part.ash, part.A, part.ldx
             else:
@@ -215,6 +297,23 @@ class DobbGroup:
             _abi._check(_abi.lib().dobb_accumulate_moment_grouped(
                 len(sub), ash, _arr([xs[i].data_ptr() for i in sub]), _abi._dtype_code(xs[sub[0]]), N, ldx,
                 float(beta), A, part.ws.data_ptr(), part.ws.numel(), sh), "dobb_accumulate_moment_grouped")
+
+    def _mx4_groups(self, part, xs):
+        """(weights, their capture shapes) of every call that takes the part's captures in MXFP4."""
+        held = [i for i in part.idx if isinstance(xs[i], Mx4Capture)]
+        for i in held:
+            if xs[i].shape[1] != self.cap_dim(i) or xs[i].device != self.device:
+                raise ValueError(f"capture {i} must hold (tokens x {self.cap_dim(i)}) on {self.device}")
+        return [(sub, [(1, self.cap_dim(i), self.nb[i]) for i in sub])
+                for sub in _split(held, lambda i: (xs[i].tiles, xs[i].shape[0]))]
+
+    def _accumulate_mx4(self, part, sh, sub, shapes, xs, beta):
+        tiles, N = xs[sub[0]].tiles, xs[sub[0]].shape[0]
+        part.ensure(_ops.dobb_moment_mx4_workspace_size(shapes, tiles))
+        _abi._check(_ops._lib().dobb_accumulate_moment_mx4_grouped(
+            len(sub), (_abi.Shape * len(sub))(*[_abi.Shape(*s) for s in shapes]), _arr([xs[i].codes.data_ptr() for i in sub]),
+            _arr([xs[i].scales.data_ptr() for i in sub]), tiles, N, float(beta), _arr([self.A[i].data_ptr() for i in sub]),
+            part.ws.data_ptr(), part.ws.numel(), sh), "dobb_accumulate_moment_mx4_grouped")
 
     def _refresh(self, part, sh, mode, iters, warm_start, tol, with_lam):
         _abi._check(_abi.lib().dobb_refresh_basis_grouped(
@@ -245,8 +344,8 @@ class DobbGroup:
 
     def accumulate(self, xs, beta: float, stream=None) -> None:
         """Capture: A_b <- beta A_b + (1-beta)/N X_b^T X_b for every weight (xs[i] is N_i x n_i, or the
-        N_i x m_i output gradients for Dobb-G)."""
-        self._grow(max(x.shape[0] for x in xs))
+        N_i x m_i output gradients for Dobb-G), as tensors or in MXFP4."""
+        self._grow(self._dense_tokens(xs))
         self._run(stream, lambda part, sh: self._accumulate(part, sh, xs, beta))
 
     def refresh(self, mode: int, iters: int, warm_start: bool = True, tol: float = 0.0, want_lambda: bool = False,
@@ -257,17 +356,28 @@ class DobbGroup:
         self._run(stream, lambda part, sh: self._refresh(part, sh, mode, iters, warm_start, tol, with_lam))
         self.refreshes += 1
 
-    def step(self, grads=None, stream=None) -> None:
+    def clip_grads(self, max_norm: float, grads=None, stream=None) -> torch.Tensor:
+        """Clip the gradients in place to a global norm over the set (dobb_clip_grad_norm_grouped); returns
+        `grad_norm`, which receives the norm before."""
         G = grads if grads is not None else self.G
+        return _ops.dobb_clip_grad_norm_grouped(G, max_norm, total=self.grad_norm, stream=stream)
+
+    def step(self, grads=None, stream=None, max_grad_norm: float | None = None) -> None:
+        G = grads if grads is not None else self.G
+        if max_grad_norm is not None:
+            self.clip_grads(max_grad_norm, G, stream)
         self._run(stream, lambda part, sh: self._step(part, sh, G))
 
     def refresh_step(self, xs, beta: float, mode: int, iters: int, grads=None, warm_start: bool = True,
-                     tol: float = 0.0, want_lambda: bool = False, stream=None) -> None:
+                     tol: float = 0.0, want_lambda: bool = False, stream=None,
+                     max_grad_norm: float | None = None) -> None:
         """accumulate, refresh and step in one call: each part runs the three phases back to back on
         its own stream, so with streams=2 one part's refresh overlaps the other's capture and step.
         The result is the same as the three calls in turn."""
-        self._grow(max(x.shape[0] for x in xs))
+        self._grow(self._dense_tokens(xs))
         G = grads if grads is not None else self.G
+        if max_grad_norm is not None:
+            self.clip_grads(max_grad_norm, G, stream)
         with_lam = want_lambda or mode == _abi.DOBB_REFRESH_EXACT
 
         def go(part, sh):
@@ -277,20 +387,21 @@ class DobbGroup:
         self._run(stream, go)
         self.refreshes += 1
 
-    def capture_refresh_step(self, xs, beta: float, mode: int, iters: int, grads=None,
-                             warm_start: bool = True) -> "torch.cuda.CUDAGraph":
+    def capture_refresh_step(self, xs, beta: float, mode: int, iters: int, grads=None, warm_start: bool = True,
+                             max_grad_norm: float | None = None) -> "torch.cuda.CUDAGraph":
         """A HIP graph of refresh_step(xs, beta, mode, iters, grads): replaying it runs the same
         kernels on the same buffers without the per-launch host work and gaps.  xs, the gradients and
         the optimizer state are bound by address, so the caller refills them in place between replays.
         Capturing runs nothing; the workspaces must already have their size, so call refresh_step once
         (or accumulate with the same token counts) first.  Each replay counts as one refresh."""
-        N = max(x.shape[0] for x in xs)
-        if N > self.n_tokens:
+        if self._dense_tokens(xs) > self.n_tokens or any(
+                part.ws.numel() < _ops.dobb_moment_mx4_workspace_size(shapes, xs[sub[0]].tiles)
+                for part in self._parts for sub, shapes in self._mx4_groups(part, xs)):
             raise RuntimeError("call refresh_step once before capturing it (the workspaces are sized there)")
         graph = torch.cuda.CUDAGraph()
         refreshes = self.refreshes
         with torch.cuda.graph(graph):
-            self.refresh_step(xs, beta, mode, iters, grads=grads, warm_start=warm_start)
+            self.refresh_step(xs, beta, mode, iters, grads=grads, warm_start=warm_start, max_grad_norm=max_grad_norm)
         self.refreshes = refreshes
         return graph
 
@@ -307,17 +418,27 @@ class Dobb(torch.optim.Optimizer):
     basis="output_gradient" runs Dobb-G (Tables 12-13): blocks of rows (m // blocks, or block_size),
     bases of the output-gradient second moment, captured by the backward hooks of
     ``attach_capture_hooks`` (or ``capture(param, grad_output)``).
+    capture_format="mx4" holds captures in MXFP4 from the moment they are taken (``Mx4Capture``): about a
+    quarter of bf16's memory between the forward pass and the refresh, and of its bytes in the refresh's
+    moment; "native" keeps the tensors.  max_grad_norm clips the gradients of this optimizer's parameters
+    in place, by their global norm, before every step; ``grad_norm`` then holds the norm before (a device
+    scalar).
     """
 
     def __init__(self, params, lr: float = 2.5e-3, weight_decay: float = 0.0, momentum: float = 0.9,
                  blocks: int = 16, block_size: int | None = None, refresh_period: int = 9, orth_iters: int = 1,
                  beta: float = 0.9, tau: float = 0.2, nesterov: bool = False, streams: int = 1,
-                 capture: str = "first", basis_dtype: torch.dtype = torch.float32, basis: str = "activation"):
+                 capture: str = "first", basis_dtype: torch.dtype = torch.float32, basis: str = "activation",
+                 capture_format: str = "native", max_grad_norm: float | None = None):
         super().__init__(params, dict(lr=lr, weight_decay=weight_decay, momentum=momentum))
         if capture not in ("first", "all"):
             raise ValueError('capture must be "first" or "all"')
         if basis not in ("activation", "output_gradient"):
             raise ValueError('basis must be "activation" (Dobb) or "output_gradient" (Dobb-G)')
+        if capture_format not in ("native", "mx4"):
+            raise ValueError('capture_format must be "native" or "mx4"')
+        if max_grad_norm is not None and not max_grad_norm >= 0:
+            raise ValueError("max_grad_norm must not be negative")
         params = [p for grp in self.param_groups for p in grp["params"]]
         for p in params:
             if p.dim() != 2:
@@ -336,6 +457,9 @@ class Dobb(torch.optim.Optimizer):
             k += len(grp["params"])
         self._applied = [None] * len(self.param_groups)
         self.capture_policy = capture
+        self.capture_format = capture_format
+        self.max_grad_norm = max_grad_norm
+        self.grad_norm: torch.Tensor | None = None
         self.T = int(refresh_period)
         self.k = int(orth_iters)
         self.beta = float(beta)
@@ -352,7 +476,7 @@ class Dobb(torch.optim.Optimizer):
         x = x.detach().reshape(-1, x.shape[-1])
         got = self._captured.setdefault(id(param), [])
         if self.capture_policy == "all" or not got:
-            got.append(x.contiguous())
+            got.append(Mx4Capture.quantize(x) if self.capture_format == "mx4" else x.contiguous())
 
     def attach_capture_hooks(self, modules):
         """Hooks on nn.Linear modules whose weights this optimizer owns: on refresh iterations their
@@ -388,12 +512,15 @@ class Dobb(torch.optim.Optimizer):
         loss = closure() if closure is not None else None
         self._sync_hparams()
         g = self._group
+        if self.max_grad_norm is not None:
+            self.grad_norm = clip_grad_norm_(self._params, self.max_grad_norm)
         grads = [p.grad if p.grad is not None else torch.zeros_like(p) for p in self._params]
         if self.wants_capture() and len(self._captured) == len(self._params):
             xs = []
             for p in self._params:
                 parts = self._captured[id(p)]
-                xs.append(parts[0] if len(parts) == 1 else torch.cat(parts, 0))
+                xs.append(Mx4Capture.cat(parts) if isinstance(parts[0], Mx4Capture) else
+                          parts[0] if len(parts) == 1 else torch.cat(parts, 0))
             if g.refreshes == 0:
                 g.refresh_step(xs, 0.0, _abi.DOBB_REFRESH_EXACT, 0, grads, warm_start=False)
             else:

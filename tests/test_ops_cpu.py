@@ -150,3 +150,17 @@ def test_python_refusals_without_a_gpu():
     with pytest.raises(ValueError, match="same number"):
         dobb.dobb_accumulate_moment_mx4_grouped([], [], [], [], 1)
     assert [dobb.mx4_tiles(n) for n in (1, 128, 129, 16384)] == [1, 1, 2, 128]
+
+
+def test_optimizer_options_are_checked():
+    from block_diagonal_eigenbasis_amd.optimizer import Dobb, clip_grad_norm_
+    w = torch.nn.Parameter(torch.zeros(4, 4))
+    with pytest.raises(ValueError, match="capture_format"):
+        Dobb([w], blocks=1, capture_format="fp4")
+    for bad in (-1.0, float("nan")):
+        with pytest.raises(ValueError, match="max_grad_norm"):
+            Dobb([w], blocks=1, max_grad_norm=bad)
+    assert float(clip_grad_norm_([w], 1.0)) == 0.0               # no gradient anywhere
+    w.grad = torch.zeros(4, 4)
+    with pytest.raises(TypeError, match="GPU tensor"):
+        clip_grad_norm_(w, 1.0)
