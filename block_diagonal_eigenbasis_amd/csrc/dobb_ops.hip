@@ -155,7 +155,7 @@ dobb_status moment_grouped(int count, const dobb_shape *shapes, const void *cons
         a.scales = ss;
         a.A = as;
         a.beta = beta;
-        a.nsplit = moment_mx4_splits(l.nb, l.blocks, tiles);
+        a.plan = moment_mx4_plan(l.nb, l.blocks, tiles);
         a.partial = (float *)ws;
         const dobb_status r = hip_status(launch_moment_mx4(a, stream));
         if (r != DOBB_OK) return r;

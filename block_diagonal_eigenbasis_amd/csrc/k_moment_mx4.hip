@@ -17,6 +17,8 @@
 //   XCD, so that its codes come from HBM once and from that XCD's L2 after that.
 // Rounding: fp32 sums of at most 4096 (narrow, then four of those in fp32) or 16384 tokens (wide) in
 // the accumulators, token splits in fp64 (k_moment_mx4_reduce).
+#include <algorithm>
+
 #include "ops_internal.h"
 
 namespace dobb {
@@ -60,24 +62,88 @@ __device__ __forceinline__ f32x16 mfma_fp4(const i32x4 &a, const i32x4 &b, f32x1
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(a), operand(b), c, 4, 4, G, (int)sa, G, (int)sb);
 }
 
-constexpr int kPairPad = 33;                   // row pitch of a 32x32 pair in LDS: rows and columns are read
+// Loads before it are all issued before anything behind it: the compiler otherwise tends to wait for
+// each load of a batch in turn, a memory latency apiece.
+__device__ __forceinline__ void batch() { __builtin_amdgcn_sched_barrier(0); }
 
-// grid: (split of block); F = ceil(nb / 32) fragments
+constexpr int kPairPad = 33;                   // row pitch of a 32x32 pair in LDS: rows and columns are read
+typedef float PairTile[32][kPairPad];
+
+// One wave: a finished 32 x 32 pair at rows i0 and columns j0 of a block, from its LDS tile.  A split's
+// partial sums leave as rows of the lower triangle; a whole sum becomes the new entries of A, rows of
+// the lower triangle and, read from the tile by columns, of the upper one.  The entries of A are read in
+// one batch, at clamped places rather than under a condition.
+__device__ __forceinline__ void store_pair(float *out, int nb, int i0, int j0, PairTile &tile, bool part, double beta, double scale) {
+    const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
+    float av[16];
+    if (!part && beta > 0.0) {
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+            const int i = min(i0 + 2 * u + half, nb - 1), j = min(j0 + col, i);
+            av[u] = out[(int64_t)i * nb + j];
+        }
+    }
+    float w[16];
+#pragma unroll
+    for (int u = 0; u < 16; ++u) w[u] = tile[2 * u + half][col];
+    batch();
+    if (!part)
+#pragma unroll
+        for (int u = 0; u < 16; ++u) w[u] = moment_out(beta, scale, av[u], (double)w[u]);
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+        const int i = i0 + 2 * u + half, j = j0 + col;
+        if (i < nb && j <= i) out[(int64_t)i * nb + j] = w[u];
+    }
+    if (part) return;
+#pragma unroll
+    for (int u = 0; u < 16; ++u) tile[2 * u + half][col] = w[u];
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int u = 0; u < 16; ++u) w[u] = tile[col][2 * u + half];
+    batch();
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+        const int i = i0 + col, j = j0 + 2 * u + half;
+        if (i < nb && j < i) out[(int64_t)j * nb + i] = w[u];
+    }
+}
+
+// Blocks 0 .. whole - 1 of a launch take their tokens in one go, the others in nsplit splits; nwg
+// workgroups each.  The first kind come first.
+struct Place {
+    int blk, split, nsplit, wg;
+};
+__device__ __forceinline__ Place place(int whole, int nsplit, int nwg) {
+    const int w = whole * nwg;
+    Place p;
+    if ((int)blockIdx.x < w) {
+        const int id = xcd_remap(blockIdx.x, w);
+        p.wg = id % nwg; p.blk = id / nwg; p.split = 0; p.nsplit = 1;
+    } else {
+        int id = xcd_remap(blockIdx.x - w, gridDim.x - w);
+        p.wg = id % nwg; id /= nwg;
+        p.split = id % nsplit; p.blk = whole + id / nsplit; p.nsplit = nsplit;
+    }
+    return p;
+}
+
+// F = ceil(nb / 32) fragments
 template <int F>
-__global__ void __launch_bounds__(256, 2) k_moment_mx4_narrow(int cnt, int nb, int64_t tiles, int nsplit, double beta, double scale,
-                                                              float *partial, MomentTable t) {
+__global__ void __launch_bounds__(256, 2) k_moment_mx4_narrow(int cnt, int nb, int64_t tiles, int whole, int nsplit_, double beta,
+                                                              double scale, float *partial, MomentTable t) {
     constexpr int PAIRS = F * (F + 1) / 2;
-    constexpr int PP = PAIRS < 2 ? 1 : 2;       // fragment pairs that are added up at a time
-    __shared__ float sm[4][PP][32][kPairPad];
+    constexpr int PH = PAIRS > 6 ? 5 : PAIRS;   // pairs that are added up at a time
+    __shared__ PairTile sm[PH][3];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int col = lane & 31, half = lane >> 5;
-    const int id = xcd_remap(blockIdx.x, gridDim.x);
-    const int blk = id / nsplit, split = id % nsplit;
+    const Place pl = place(whole, nsplit_, 1);
+    const int blk = pl.blk;
     const int mat = find_matrix(t, cnt, blk);
     const int64_t n = t.n[mat];
     const int64_t tp = (tiles + 1) / 2;
-    const int64_t per = (tp + nsplit - 1) / nsplit;
-    const int64_t p0 = per * split, p1 = p0 + per < tp ? p0 + per : tp;
+    const int64_t per = (tp + pl.nsplit - 1) / pl.nsplit;
+    const int64_t p0 = per * pl.split, p1 = p0 + per < tp ? p0 + per : tp;
     const int64_t cb = (int64_t)(blk - t.first[mat]) * nb;
     const i32x4 *codes = t.codes[mat] + cb;
     const uint32_t *scales = t.scales[mat] + cb;
@@ -116,57 +182,37 @@ __global__ void __launch_bounds__(256, 2) k_moment_mx4_narrow(int cnt, int nb, i
 #undef DOBB_MX4_GROUP
     }
 
-    // out: the split's partial sums, or A with both its triangles.  Thread t has column t % 32 and rows
-    // t / 32 + 8 u of every pair; its entries of A are on their way while the waves' sums are added.
+    // Pair p ends up with wave p % 4: the others hand it their sums through LDS, and it adds them in
+    // the order of the waves behind it and stores the pair.
     const int64_t nbb = (int64_t)nb * nb;
-    float *out = nsplit > 1 ? partial + ((int64_t)blk * nsplit + split) * nbb : t.A[mat] + (blk - t.first[mat]) * nbb;
-    const int tr = threadIdx.x >> 5, tc = threadIdx.x & 31;
-    const bool old = nsplit == 1 && beta > 0.0;
-    float av[PAIRS][4];
-    if (old) {
-        int q = 0;
+    const bool part = pl.nsplit > 1;
+    float *out = part ? partial + ((int64_t)(blk - whole) * pl.nsplit + pl.split) * nbb : t.A[mat] + (blk - t.first[mat]) * nbb;
 #pragma unroll
-        for (int fi = 0; fi < F; ++fi)
+    for (int h = 0; h < PAIRS; h += PH) {
+        if (h > 0) __syncthreads();
 #pragma unroll
-            for (int fj = 0; fj <= fi; ++fj, ++q)
+        for (int p = h; p < h + PH && p < PAIRS; ++p)
+            if (wave != p % 4)
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int i = min(32 * fi + tr + 8 * u, nb - 1), j = min(32 * fj + tc, i);   // no branches
-                    av[q][u] = out[(int64_t)i * nb + j];
-                }
-    }
-#pragma unroll
-    for (int q0 = 0; q0 < PAIRS; q0 += PP) {
-        if (q0 > 0) __syncthreads();
-#pragma unroll
-        for (int q = q0; q < q0 + PP && q < PAIRS; ++q)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) sm[wave][q - q0][acc_row(r, lane)][col] = acc[q][r];
+                for (int r = 0; r < 16; ++r) sm[p - h][(wave + 3 - p) & 3][acc_row(r, lane)][col] = acc[p][r];
         __syncthreads();
 #pragma unroll
-        for (int q = q0; q < q0 + PP && q < PAIRS; ++q) {
-            int fi = 0, fj = q;
-            while (fj > fi) fj -= ++fi;
+        for (int p = h; p < h + PH && p < PAIRS; ++p)
+            if (wave == p % 4) {
+                float x[3][16];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int r = tr + 8 * u, i = 32 * fi + r, j = 32 * fj + tc;
-                const float sum = ((sm[0][q - q0][r][tc] + sm[1][q - q0][r][tc]) + sm[2][q - q0][r][tc]) + sm[3][q - q0][r][tc];
-                const float v = nsplit > 1 ? sum : moment_out(beta, scale, old ? av[q][u] : 0.f, (double)sum);
-                if (i < nb && j <= i) out[(int64_t)i * nb + j] = v;
-                sm[0][q - q0][r][tc] = v;       // read by this thread only, until the barrier
+                for (int k = 0; k < 3; ++k)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) x[k][r] = sm[p - h][k][acc_row(r, lane)][col];
+                batch();
+#pragma unroll
+                for (int r = 0; r < 16; ++r) sm[p - h][0][acc_row(r, lane)][col] = ((acc[p][r] + x[0][r]) + x[1][r]) + x[2][r];
             }
-        }
-        if (nsplit > 1) continue;
-        __syncthreads();
-#pragma unroll
-        for (int q = q0; q < q0 + PP && q < PAIRS; ++q) {
-            int fi = 0, fj = q;
-            while (fj > fi) fj -= ++fi;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {       // the mirrored entries, rows of the upper triangle
-                const int c = tr + 8 * u, i = 32 * fi + tc, j = 32 * fj + c;
-                if (i < nb && j < i) out[(int64_t)j * nb + i] = sm[0][q - q0][tc][c];
-            }
+        int fi = 0, fj = 0;
+#pragma unroll 1
+        for (int p = 0; p < h + PH && p < PAIRS; ++p) {
+            if (p >= h && wave == p % 4) store_pair(out, nb, 32 * fi, 32 * fj, sm[p - h][0], part, beta, scale);
+            if (++fj > fi) { fj = 0; ++fi; }
         }
     }
 }
@@ -181,21 +227,20 @@ __host__ __device__ inline int wide_groups(int F) {
 }
 
 // GS groups of the tile pair a stage (4, or 2 where four stages of 4 would not fit the LDS); PT 16-byte
-// pieces of a stage a thread, ST scale words.  grid: (workgroup of split of block)
+// pieces of a stage a thread, ST scale words
 template <int GS, int PT, int ST>
-__global__ void __launch_bounds__(kWideThreads, 2) k_moment_mx4_wide(int cnt, int nb, int F, int nwg, int64_t tiles, int nsplit,
-                                                                     double beta, double scale, float *partial, MomentTable t) {
+__global__ void __launch_bounds__(kWideThreads, 2) k_moment_mx4_wide(int cnt, int nb, int F, int nwg, int64_t tiles, int whole,
+                                                                     int nsplit_, double beta, double scale, float *partial, MomentTable t) {
     extern __shared__ __align__(16) unsigned char lds[];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int col = lane & 31, half = lane >> 5;
-    int id = xcd_remap(blockIdx.x, gridDim.x);
-    const int wg = id % nwg; id /= nwg;
-    const int split = id % nsplit, blk = id / nsplit;
+    const Place pl = place(whole, nsplit_, nwg);
+    const int wg = pl.wg, blk = pl.blk;
     const int mat = find_matrix(t, cnt, blk);
     const int64_t n = t.n[mat];
     const int64_t tp = (tiles + 1) / 2;
-    const int64_t per = (tp + nsplit - 1) / nsplit;
-    const int64_t p0 = per * split, p1 = p0 + per < tp ? p0 + per : tp;
+    const int64_t per = (tp + pl.nsplit - 1) / pl.nsplit;
+    const int64_t p0 = per * pl.split, p1 = p0 + per < tp ? p0 + per : tp;
     const int64_t cb = (int64_t)(blk - t.first[mat]) * nb;
     const char *codes = (const char *)(t.codes[mat] + cb);
     const uint32_t *scales = t.scales[mat] + cb;
@@ -301,61 +346,75 @@ __global__ void __launch_bounds__(kWideThreads, 2) k_moment_mx4_wide(int cnt, in
         __syncthreads();
     }
     if (I < 0) return;
-    // every pair leaves as rows of the lower triangle and, through a tile of LDS of the wave's own, of the
-    // upper one; its 16 entries of A a lane are read before anything of it is written
+    // the pairs leave through a tile of LDS of the wave's own, in a rolled loop (unrolled, the stores
+    // were two thirds of the kernel's code)
     const int64_t nbb = (int64_t)nb * nb;
-    float *out = nsplit > 1 ? partial + ((int64_t)blk * nsplit + split) * nbb : t.A[mat] + (blk - t.first[mat]) * nbb;
-    float (*tile)[kPairPad] = (float (*)[kPairPad])(lds + wave * sizeof(float) * 32 * kPairPad);
+    const bool part = pl.nsplit > 1;
+    float *out = part ? partial + ((int64_t)(blk - whole) * pl.nsplit + pl.split) * nbb : t.A[mat] + (blk - t.first[mat]) * nbb;
+    PairTile &tile = *(PairTile *)(lds + wave * sizeof(PairTile));
+#pragma unroll 1
+    for (int p = 0; p < 8; ++p) {
+        const int i0 = 32 * (2 * I + (p >> 2)), j0 = 32 * (4 * J + (p & 3));
+        if (i0 >= nb || j0 > i0) continue;
 #pragma unroll
-    for (int fi = 0; fi < 2; ++fi)
+        for (int q = 0; q < 8; ++q)
+            if (q == p)
 #pragma unroll
-        for (int fj = 0; fj < 4; ++fj) {
-            const int i0 = 32 * (2 * I + fi), j0 = 32 * (4 * J + fj);
-            if (i0 >= nb || j0 > i0) continue;
-            float av[16];
-            if (nsplit == 1 && beta > 0.0) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int i = min(i0 + acc_row(r, lane), nb - 1), j = min(j0 + col, i);   // no branches
-                    av[r] = out[(int64_t)i * nb + j];
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int i = i0 + acc_row(r, lane), j = j0 + col;
-                const float w = nsplit > 1 ? acc[fi][fj][r] : moment_out(beta, scale, av[r], (double)acc[fi][fj][r]);
-                if (i < nb && j <= i) out[(int64_t)i * nb + j] = w;
-                if (nsplit == 1) tile[acc_row(r, lane)][col] = w;
-            }
-            if (nsplit > 1) continue;
-            __builtin_amdgcn_wave_barrier();
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int c = 2 * r + half, i = i0 + col, j = j0 + c;
-                const float w = tile[col][c];
-                if (i < nb && j < i) out[(int64_t)j * nb + i] = w;
-            }
-            __builtin_amdgcn_wave_barrier();
-        }
+                for (int r = 0; r < 16; ++r) tile[acc_row(r, lane)][col] = acc[q >> 2][q & 3][r];
+        __builtin_amdgcn_wave_barrier();
+        store_pair(out, nb, i0, j0, tile, part, beta, scale);
+        __builtin_amdgcn_wave_barrier();
+    }
 }
 
-// one thread per entry on or below the diagonal: the splits' sums in fp64, in split order
-__global__ void __launch_bounds__(256) k_moment_mx4_reduce(int cnt, int nb, int nsplit, int chunks, double beta, double scale,
-                                                           const float *partial, MomentTable t) {
+// The splits' sums of one 32 x 32 pair in fp64, in split order, for blocks whole .. of a launch; one
+// workgroup a pair, thread t with column t % 32 and rows t / 32 + 8 u
+__global__ void __launch_bounds__(256) k_moment_mx4_reduce(int cnt, int nb, int whole, int nsplit, int pairs, double beta,
+                                                           double scale, const float *partial, MomentTable t) {
+    __shared__ PairTile tile;
     const int64_t nbb = (int64_t)nb * nb;
-    const int blk = blockIdx.x / chunks;
-    const int64_t at = (int64_t)(blockIdx.x % chunks) * 256 + threadIdx.x;
-    if (at >= nbb) return;
-    const int i = (int)(at / nb), j = (int)(at % nb);
-    if (j > i) return;
-    const float *p = partial + (int64_t)blk * nsplit * nbb + at;
-    double s = 0.0;
-    for (int k = 0; k < nsplit; ++k) s += (double)p[k * nbb];
+    const int blk = whole + blockIdx.x / pairs;
+    int fi = 0, fj = blockIdx.x % pairs;
+    while (fj > fi) fj -= ++fi;
     const int mat = find_matrix(t, cnt, blk);
     float *A = t.A[mat] + (blk - t.first[mat]) * nbb;
-    const float v = moment_out(beta, scale, beta > 0.0 ? A[at] : 0.f, s);
-    A[at] = v;
-    if (i != j) A[(int64_t)j * nb + i] = v;
+    const float *p = partial + (int64_t)(blk - whole) * nsplit * nbb;
+    const int tr = threadIdx.x >> 5, tc = threadIdx.x & 31;
+    int64_t at[4];
+    float av[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int i = min(32 * fi + tr + 8 * u, nb - 1), j = min(32 * fj + tc, i);   // no branches
+        at[u] = (int64_t)i * nb + j;
+        if (beta > 0.0) av[u] = A[at[u]];
+    }
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
+    for (int k0 = 0; k0 < nsplit; k0 += 4) {
+        float x[4][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) x[k][u] = p[min(k0 + k, nsplit - 1) * nbb + at[u]];
+        batch();
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k0 + k < nsplit)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) s[u] += (double)x[k][u];
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int r = tr + 8 * u, i = 32 * fi + r, j = 32 * fj + tc;
+        const float v = moment_out(beta, scale, av[u], s[u]);
+        if (i < nb && j <= i) A[at[u]] = v;
+        tile[r][tc] = v;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int c = tr + 8 * u, i = 32 * fi + tc, j = 32 * fj + c;
+        if (i < nb && j < i) A[(int64_t)j * nb + i] = tile[tc][c];
+    }
 }
 
 int wide_wgs(int64_t nb) { return (wide_groups((int)(nb + 31) / 32) + 7) / 8; }
@@ -365,39 +424,57 @@ hipError_t launch_wide(const MomentMx4Args &a, const MomentTable &t, unsigned gr
     const size_t lds = 2 * ((size_t)GS * 1024 * F + 256 * (size_t)F);
     (void)hipFuncSetAttribute((const void *)k_moment_mx4_wide<GS, PT, ST>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     DOBB_LAUNCH("moment_mx4_wide", s, (k_moment_mx4_wide<GS, PT, ST>), dim3(grid), dim3(kWideThreads), lds, a.count, (int)a.nb, F, nwg,
-                a.tiles, a.nsplit, (double)a.beta, scale, a.partial, t);
+                a.tiles, a.plan.whole, a.plan.nsplit, (double)a.beta, scale, a.partial, t);
     return hipGetLastError();
 }
 
 }  // namespace
 
-// Token splits of one launch over `blocks` blocks: the number that an estimate of the time makes
-// smallest.  A split count costs rounds of workgroups over the chip's slots (two narrow workgroups or
-// one wide one a CU) of so many tile pairs each, at 0.6 us (narrow: four at once) or 1.2 us (wide), and
-// more than one split costs the partial sums' traffic and the reduction's launch.  Never more tile pairs
-// than kSplitPairs a split, never a split with none.
-int moment_mx4_splits(int64_t nb, int64_t blocks, int64_t tiles) {
+// How a launch over `blocks` blocks splits their tokens: the plan that an estimate of the time makes
+// smallest.  A launch runs in rounds of workgroups over the chip's slots (two narrow workgroups or one
+// wide one a CU); a tile pair takes a workgroup about 0.6 us (narrow; 1.4 us and more where all slots
+// read at once) or 2.2 us (wide).  Whole rounds of blocks are left whole; those of the last round, which
+// would leave slots empty, may be split, for the partial sums' traffic and a launch of 6 us.  Never more
+// tile pairs than kSplitPairs in one go, never a split with none.
+MomentPlan moment_mx4_plan(int64_t nb, int64_t blocks, int64_t tiles) {
     const int64_t tp = (tiles + 1) / 2;
     const bool narrow = nb <= kNarrow;
-    const int64_t units = blocks * (narrow ? 1 : wide_wgs(nb)), slots = narrow ? 512 : 256;
-    const double tau = narrow ? 0.15 : 1.2, partial = (double)blocks * nb * nb * 8 / 5e6;
+    const int64_t nwg = narrow ? 1 : wide_wgs(nb), slots = narrow ? 512 : 256;
+    const double partial = (double)nb * nb * 8 / 5e6;
+    auto run = [&](int64_t wgs, int64_t pairs) {           // us of wgs workgroups of so many tile pairs
+        double t = 0.0;
+        for (; wgs > 0; wgs -= std::min(wgs, slots)) {
+            const double full = (double)std::min(wgs, slots) / 512 * 1.8 * nb / 128;
+            t += narrow ? std::max({0.6 * ((pairs + 3) / 4) * 4, full * pairs, 2.4}) : 2.2 * pairs;
+            if (wgs > 64 * slots) return t * (double)wgs / slots;
+        }
+        return t;
+    };
     const int64_t least = (tp + kSplitPairs - 1) / kSplitPairs;
-    int64_t best = least;
+    MomentPlan best{0, 1};
     double cost = 1e300;
-    for (int64_t ns = least; ns <= tp && ns <= least + 64; ++ns) {
-        const int64_t per = (tp + ns - 1) / ns;
-        if ((tp + per - 1) / per != ns) continue;
-        const double c = (double)((units * ns + slots - 1) / slots) * (narrow ? (per + 3) / 4 * 4 : per) * tau +
-                         (ns > 1 ? 6.0 + partial * (double)ns : 0.0);
-        if (c < cost) { best = ns; cost = c; }
+    const int64_t full = blocks * nwg / slots * slots / nwg;
+    for (const int64_t whole : {blocks, full, (int64_t)0}) {
+        if (whole > 0 && least > 1) continue;
+        const int64_t rest = blocks - whole;
+        for (int64_t ns = least; ns <= tp && ns <= least + 63; ++ns) {
+            const int64_t per = (tp + ns - 1) / ns;
+            if ((tp + per - 1) / per != ns) continue;
+            const double c = run(whole * nwg, tp) + (rest ? run(rest * nwg * ns, per) : 0.0) +
+                             (rest && ns > 1 ? 6.0 + partial * (double)(rest * ns) : 0.0);
+            if (c < cost) { best = rest && ns > 1 ? MomentPlan{(int)whole, (int)ns} : MomentPlan{(int)blocks, 1}; cost = c; }
+        }
     }
-    const int64_t per = (tp + best - 1) / best;
-    return (int)((tp + per - 1) / per);
+    if (cost == 1e300) {                                   // no even count of splits in the range
+        const int64_t per = (tp + least - 1) / least;
+        best = {0, (int)((tp + per - 1) / per)};
+    }
+    return best;
 }
 
 size_t moment_mx4_ws(int64_t nb, int64_t blocks, int64_t tiles) {
-    const int ns = moment_mx4_splits(nb, blocks, tiles);
-    return ns > 1 ? (size_t)blocks * (size_t)nb * (size_t)nb * 4 * (size_t)ns : 0;
+    const MomentPlan p = moment_mx4_plan(nb, blocks, tiles);
+    return (size_t)(blocks - p.whole) * (size_t)nb * (size_t)nb * 4 * (size_t)p.nsplit;
 }
 
 hipError_t launch_moment_mx4(const MomentMx4Args &a, hipStream_t s) {
@@ -415,14 +492,15 @@ hipError_t launch_moment_mx4(const MomentMx4Args &a, hipStream_t s) {
     t.first[a.count] = (int32_t)blocks;
     const int nb = (int)a.nb, F = (nb + 31) / 32;
     const int nwg = nb <= kNarrow ? 1 : wide_wgs(nb);
-    const int64_t chunks = (a.nb * a.nb + 255) / 256;
-    if (blocks * a.nsplit * nwg > 0x7fffffff || blocks * chunks > 0x7fffffff) return hipErrorInvalidValue;
+    const int64_t rest = blocks - a.plan.whole, pairs = (int64_t)F * (F + 1) / 2;
+    const int64_t wgs = (a.plan.whole + rest * a.plan.nsplit) * nwg;
+    if (a.plan.whole < 0 || rest < 0 || wgs > 0x7fffffff || rest * pairs > 0x7fffffff) return hipErrorInvalidValue;
     const double scale = (1.0 - (double)a.beta) / (double)a.N;
-    const unsigned grid = (unsigned)(blocks * a.nsplit * nwg);
+    const unsigned grid = (unsigned)wgs;
     hipError_t e = hipSuccess;
 #define DOBB_MX4_NARROW(F)                                                                                             \
-    DOBB_LAUNCH("moment_mx4_narrow", s, k_moment_mx4_narrow<F>, dim3(grid), dim3(256), 0, a.count, nb, a.tiles, a.nsplit, \
-                (double)a.beta, scale, a.partial, t)
+    DOBB_LAUNCH("moment_mx4_narrow", s, k_moment_mx4_narrow<F>, dim3(grid), dim3(256), 0, a.count, nb, a.tiles, a.plan.whole, \
+                a.plan.nsplit, (double)a.beta, scale, a.partial, t)
     if (F == 1) DOBB_MX4_NARROW(1);
     else if (F == 2) DOBB_MX4_NARROW(2);
     else if (F == 3) DOBB_MX4_NARROW(3);
@@ -434,9 +512,9 @@ hipError_t launch_moment_mx4(const MomentMx4Args &a, hipStream_t s) {
     else if (F <= 16) e = launch_wide<4, 8, 2>(a, t, grid, F, nwg, scale, s);
     else e = launch_wide<2, 8, 4>(a, t, grid, F, nwg, scale, s);
     if (e == hipSuccess) e = hipGetLastError();
-    if (e != hipSuccess || a.nsplit == 1) return e;
-    DOBB_LAUNCH("moment_mx4_reduce", s, k_moment_mx4_reduce, dim3((unsigned)(blocks * chunks)), dim3(256), 0, a.count, nb, a.nsplit,
-                (int)chunks, (double)a.beta, scale, a.partial, t);
+    if (e != hipSuccess || rest == 0) return e;
+    DOBB_LAUNCH("moment_mx4_reduce", s, k_moment_mx4_reduce, dim3((unsigned)(rest * pairs)), dim3(256), 0, a.count, nb, a.plan.whole,
+                a.plan.nsplit, (int)pairs, (double)a.beta, scale, a.partial, t);
     return hipGetLastError();
 }
 

@@ -26,6 +26,9 @@ hipError_t launch_mx4_dequantize(int64_t N, int64_t n, const void *codes, const 
                                  int64_t ldo, hipStream_t s);
 
 constexpr int kMomentMats = 96;       // matrices of one launch
+struct MomentPlan {
+    int whole, nsplit;                // blocks 0 .. whole - 1 unsplit, the others in nsplit token splits
+};
 struct MomentMx4Args {
     int count;                        // matrices with blocks of one width; at most kMomentMats
     int64_t nb, tiles, N;
@@ -34,10 +37,10 @@ struct MomentMx4Args {
     const void *const *scales;
     float *const *A;
     float beta;
-    int nsplit;
-    float *partial;                   // nsplit > 1: blocks x nsplit x nb x nb
+    MomentPlan plan;
+    float *partial;                   // (blocks - whole) x nsplit x nb x nb
 };
-int moment_mx4_splits(int64_t nb, int64_t blocks, int64_t tiles);
+MomentPlan moment_mx4_plan(int64_t nb, int64_t blocks, int64_t tiles);
 size_t moment_mx4_ws(int64_t nb, int64_t blocks, int64_t tiles);
 hipError_t launch_moment_mx4(const MomentMx4Args &a, hipStream_t s);
 
