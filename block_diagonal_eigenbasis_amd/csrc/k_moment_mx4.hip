@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(256, 2) k_moment_mx4_narrow(int cnt, int nb, i
     constexpr int PAIRS = F * (F + 1) / 2;
     constexpr int PH = PAIRS > 6 ? 5 : PAIRS;   // pairs that are added up at a time
     __shared__ PairTile sm[PH][3];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 31, half = lane >> 5;
     const Place pl = place(whole, nsplit_, 1);
     const int blk = pl.blk;
@@ -145,42 +145,68 @@ __global__ void __launch_bounds__(256, 2) k_moment_mx4_narrow(int cnt, int nb, i
     const int64_t per = (tp + pl.nsplit - 1) / pl.nsplit;
     const int64_t p0 = per * pl.split, p1 = p0 + per < tp ? p0 + per : tp;
     const int64_t cb = (int64_t)(blk - t.first[mat]) * nb;
-    const i32x4 *codes = t.codes[mat] + cb;
-    const uint32_t *scales = t.scales[mat] + cb;
-    // columns past the block repeat its last one: they fill rows and columns that are not written
+    const char *codes = (const char *)(t.codes[mat] + cb);
+    const char *scales = (const char *)(t.scales[mat] + cb);
+    // byte offsets of this lane's fragment columns (columns past the block repeat its last one: they fill
+    // rows and columns that are not written) and of its half's tile
     uint32_t ci[F];
 #pragma unroll
-    for (int f = 0; f < F; ++f) ci[f] = 32 * f + col < nb ? 32 * f + col : nb - 1;
+    for (int f = 0; f < F; ++f) ci[f] = (uint32_t)(32 * f + col < nb ? 32 * f + col : nb - 1) * 4;
+    const uint32_t tile_b = half ? (uint32_t)(64 * n) : 0u;
     f32x16 acc[PAIRS];
 #pragma unroll
     for (int p = 0; p < PAIRS; ++p) acc[p] = f32x16{};
 
-    for (int64_t p = p0 + wave; p < p1; p += 4) {
-        const int64_t tl = 2 * p + half;
-        const bool in = tl < tiles;             // an odd last tile: the other half's scales become 2^-127,
-        const int64_t tt = in ? tl : tiles - 1; // whose products vanish in fp32
-        const i32x4 *cp = codes + tt * 4 * n;
-        const uint32_t *sp = scales + tt * n;
-        uint32_t sa[F];
-        i32x4 a[4][F];
+    // A wave's operands are one tile pair ahead: once the products of a group are on their way, its
+    // registers take the next pair's group, so loads are in flight all the time.
+    uint32_t sa[F], sn[F];
+    i32x4 a[4][F];
+    const char *cp = nullptr;                   // of the pair that is being loaded
+    uint32_t mine = 0;
+    bool in = true;
+    auto load_scales = [&](int64_t p) {
+        const bool odd = 2 * p + 1 >= tiles;    // an odd last tile: the other half reads it too, and its
+        in = !(odd && half);                    // scales become 2^-127, whose products vanish in fp32
+        mine = odd ? 0u : tile_b;
+        cp = codes + 2 * p * (64 * n);
+        const char *sp = scales + 2 * p * (4 * n);
 #pragma unroll
-        for (int f = 0; f < F; ++f) sa[f] = sp[ci[f]];
+        for (int f = 0; f < F; ++f) sn[f] = *(const uint32_t *)(sp + (mine / 16 + ci[f]));
+    };
+    auto load_group = [&](int g) {
+        const char *gp = cp + g * (16 * n);
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
+        for (int f = 0; f < F; ++f) a[g][f] = *(const i32x4 *)(gp + (mine + 4 * ci[f]));
+    };
+    auto take_scales = [&]() {
 #pragma unroll
-            for (int f = 0; f < F; ++f) a[g][f] = cp[g * n + ci[f]];
-#pragma unroll
-        for (int f = 0; f < F; ++f) sa[f] = in ? sa[f] : 0u;
-#define DOBB_MX4_GROUP(g)                                                          \
-        {                                                                          \
-            int q = 0;                                                             \
-            _Pragma("unroll") for (int i = 0; i < F; ++i)                          \
-                _Pragma("unroll") for (int j = 0; j <= i; ++j, ++q)                \
-                    acc[q] = mfma_fp4<g>(a[g][i], a[g][j], acc[q], sa[i], sa[j]);  \
-        }
-        DOBB_MX4_GROUP(0) DOBB_MX4_GROUP(1) DOBB_MX4_GROUP(2) DOBB_MX4_GROUP(3)
-#undef DOBB_MX4_GROUP
+        for (int f = 0; f < F; ++f) sa[f] = in ? sn[f] : 0u;
+    };
+#define DOBB_MX4_GROUP(g, NEXT)                                                \
+    {                                                                          \
+        int q = 0;                                                             \
+        _Pragma("unroll") for (int i = 0; i < F; ++i)                          \
+            _Pragma("unroll") for (int j = 0; j <= i; ++j, ++q)                \
+                acc[q] = mfma_fp4<g>(a[g][i], a[g][j], acc[q], sa[i], sa[j]);  \
+        batch();                                                               \
+        if (NEXT) load_group(g);                                               \
+        batch();                                                               \
     }
+    int64_t p = p0 + wave;
+    if (p < p1) {
+        load_scales(p);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) load_group(g);
+        batch();
+        for (; p + 4 < p1; p += 4) {
+            take_scales();
+            load_scales(p + 4);
+            DOBB_MX4_GROUP(0, true) DOBB_MX4_GROUP(1, true) DOBB_MX4_GROUP(2, true) DOBB_MX4_GROUP(3, true)
+        }
+        take_scales();
+        DOBB_MX4_GROUP(0, false) DOBB_MX4_GROUP(1, false) DOBB_MX4_GROUP(2, false) DOBB_MX4_GROUP(3, false)
+    }
+#undef DOBB_MX4_GROUP
 
     // Pair p ends up with wave p % 4: the others hand it their sums through LDS, and it adds them in
     // the order of the waves behind it and stores the pair.
