@@ -21,35 +21,52 @@ struct __attribute__((packed, aligned(2))) Pair { uint32_t w[BF16 ? 1 : 2]; };
 __device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 template <bool BF16>
-__global__ void __launch_bounds__(256) k_mx4_quantize(int64_t N, int64_t n, int64_t ldx, int64_t colblocks, const void *X,
+__global__ void __launch_bounds__(256) k_mx4_quantize(int64_t N, int64_t n, int64_t ldx, unsigned colblocks, const void *X,
                                                       uint4 *codes, uint32_t *scales) {
     __shared__ uint8_t sc[kCols][4];
     const int64_t tile = blockIdx.x / colblocks;
-    const int64_t c0 = (blockIdx.x % colblocks) * kCols;
-    const int g = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t c0 = (int64_t)(blockIdx.x % colblocks) * kCols;
+    const int g = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int64_t c = c0 + 2 * lane;
     const int64_t t0 = tile * kMx4Tile + 32 * g;
     const int rows = N - t0 < 0 ? 0 : N - t0 < 32 ? (int)(N - t0) : 32;
+    // Every load is in bounds and unconditional (a condition would wait for each in turn): rows past the
+    // last token repeat it and become zeros below, a pair past the last column moves to the last two.
     constexpr int ES = BF16 ? 2 : 4;
-    const char *x = (const char *)X + ((t0 < N ? t0 : 0) * ldx + c) * ES;
+    const uint32_t xc = (uint32_t)(c + 1 < n ? c : n > 1 ? n - 2 : 0) * ES;
+    const char *x = (const char *)X + (t0 < N ? t0 : 0) * ldx * ES;   // the same for the wave: rows by scalar address
     float a[32], b[32];
-    if (c + 1 < n && rows == 32) {
-        Pair<BF16> v[32];
+    if (rows == 0) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] = *(const Pair<BF16> *)(x + k * ldx * ES);
+        for (int k = 0; k < 32; ++k) a[k] = b[k] = 0.f;
+    } else {
+        Pair<BF16> v[32];
+        if (n > 1) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = *(const Pair<BF16> *)(x + min(k, rows - 1) * ldx * ES + xc);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+                const char *r = x + min(k, rows - 1) * ldx * ES + xc;
+                v[k].w[0] = BF16 ? *(const uint16_t *)r : *(const uint32_t *)r;
+                if (!BF16) v[k].w[BF16 ? 0 : 1] = 0;
+            }
+        }
+        const bool last = n > 1 && c + 1 >= n;              // the pair's second column is this lane's first
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
             a[k] = BF16 ? __uint_as_float(v[k].w[0] << 16) : __uint_as_float(v[k].w[0]);
             b[k] = BF16 ? __uint_as_float(v[k].w[0] & 0xffff0000u) : __uint_as_float(v[k].w[BF16 ? 0 : 1]);
         }
-    } else {
+        if (last)
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-            const bool in = k < rows;
-            const char *r = x + k * ldx * ES;
-            a[k] = in && c < n ? (BF16 ? bf16_to_f32(*(const uint16_t *)r) : *(const float *)r) : 0.f;
-            b[k] = in && c + 1 < n ? (BF16 ? bf16_to_f32(*(const uint16_t *)(r + ES)) : *(const float *)(r + ES)) : 0.f;
-        }
+            for (int k = 0; k < 32; ++k) a[k] = b[k];
+        if (rows < 32)
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+                a[k] = k < rows ? a[k] : 0.f;
+                b[k] = k < rows ? b[k] : 0.f;
+            }
     }
     uint32_t ma = 0, mb = 0;
 #pragma unroll
@@ -90,11 +107,11 @@ __global__ void __launch_bounds__(256) k_mx4_quantize(int64_t N, int64_t n, int6
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 template <bool BF16>
-__global__ void __launch_bounds__(256) k_mx4_dequantize(int64_t N, int64_t n, int64_t ldo, int64_t colblocks, const uint4 *codes,
+__global__ void __launch_bounds__(256) k_mx4_dequantize(int64_t N, int64_t n, int64_t ldo, unsigned colblocks, const uint4 *codes,
                                                         const uint8_t *scales, void *out) {
     const int64_t tile = blockIdx.x / colblocks;
-    const int64_t c0 = (blockIdx.x % colblocks) * kCols;
-    const int g = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t c0 = (int64_t)(blockIdx.x % colblocks) * kCols;
+    const int g = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int64_t c = c0 + 2 * lane;
     const int64_t t0 = tile * kMx4Tile + 32 * g;
     if (c >= n || t0 >= N) return;
@@ -108,7 +125,8 @@ __global__ void __launch_bounds__(256) k_mx4_dequantize(int64_t N, int64_t n, in
     const float sa = __uint_as_float(ea << 23), sb = __uint_as_float(eb << 23);
     const uint32_t wa[4] = {ca.x, ca.y, ca.z, ca.w}, wb[4] = {cb.x, cb.y, cb.z, cb.w};
     constexpr int ES = BF16 ? 2 : 4;
-    char *o = (char *)out + (t0 * ldo + c) * ES;
+    char *o = (char *)out + t0 * ldo * ES;
+    const uint32_t oc = (uint32_t)c * ES;
     float a[32], b[32];
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
@@ -130,7 +148,7 @@ __global__ void __launch_bounds__(256) k_mx4_dequantize(int64_t N, int64_t n, in
 #pragma unroll
     for (int k = 0; k < 32; ++k) {
         if (k >= rows) break;
-        char *r = o + k * ldo * ES;
+        char *r = o + k * ldo * ES + oc;
         if (two) {
             Pair<BF16> v;
             if (BF16) v.w[0] = (uint32_t)f32_to_bf16(a[k]) | ((uint32_t)f32_to_bf16(b[k]) << 16);
@@ -142,8 +160,8 @@ __global__ void __launch_bounds__(256) k_mx4_dequantize(int64_t N, int64_t n, in
 }
 
 // workgroups of a capture, 0 if a grid cannot hold them
-unsigned mx4_grid(int64_t N, int64_t n, int64_t *colblocks) {
-    *colblocks = (n + kCols - 1) / kCols;
+unsigned mx4_grid(int64_t N, int64_t n, unsigned *colblocks) {
+    *colblocks = (unsigned)((n + kCols - 1) / kCols);
     const int64_t tiles = N / kMx4Tile + (N % kMx4Tile != 0);
     if (tiles > 0x7fffffff / *colblocks) return 0;
     return (unsigned)(tiles * *colblocks);
@@ -153,7 +171,7 @@ unsigned mx4_grid(int64_t N, int64_t n, int64_t *colblocks) {
 
 hipError_t launch_mx4_quantize(int64_t N, int64_t n, const void *X, bool bf16, int64_t ldx, void *codes, void *scales,
                                hipStream_t s) {
-    int64_t cb;
+    unsigned cb;
     const unsigned grid = mx4_grid(N, n, &cb);
     if (!grid) return hipErrorInvalidValue;
     if (bf16) DOBB_LAUNCH("mx4_quantize", s, k_mx4_quantize<true>, dim3(grid), dim3(256), 0, N, n, ldx, cb, X, (uint4 *)codes, (uint32_t *)scales);
@@ -163,7 +181,7 @@ hipError_t launch_mx4_quantize(int64_t N, int64_t n, const void *X, bool bf16, i
 
 hipError_t launch_mx4_dequantize(int64_t N, int64_t n, const void *codes, const void *scales, void *out, bool bf16,
                                  int64_t ldo, hipStream_t s) {
-    int64_t cb;
+    unsigned cb;
     const unsigned grid = mx4_grid(N, n, &cb);
     if (!grid) return hipErrorInvalidValue;
     if (bf16) DOBB_LAUNCH("mx4_dequantize", s, k_mx4_dequantize<true>, dim3(grid), dim3(256), 0, N, n, ldo, cb, (const uint4 *)codes, (const uint8_t *)scales, out);
