@@ -17,8 +17,70 @@ constexpr int kCols = 128;   // columns per workgroup
 template <bool BF16>
 struct __attribute__((packed, aligned(2))) Pair { uint32_t w[BF16 ? 1 : 2]; };
 
-// the largest magnitude's bits, as fp32: its exponent field is bits >> 23, from 255 on not finite
-__device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// The scale byte of a group from its largest magnitude's exponent field: two below it, 255 if not finite
+__device__ __forceinline__ uint32_t scale_byte(uint32_t field) { return field == 255 ? 255u : field < 2 ? 0u : field - 2; }
+// the scale as the conversions take it: its byte is the exponent field, 0 stands for 2^-127
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+
+// 32 tokens of two neighbouring columns: scale bytes and codes.  The largest magnitudes are found as
+// integers (a NaN's bits are above an infinity's).  In bf16 both columns' at once in packed 16-bit
+// integers, and one byte permute pairs two tokens of a column for the conversion from bf16: about half the
+// vector instructions of going through fp32.
+template <bool BF16>
+__device__ __forceinline__ void quantize_pair(const Pair<BF16> (&v)[32], uint32_t &ea, uint32_t &eb, uint32_t (&qa)[4], uint32_t (&qb)[4]) {
+    if constexpr (BF16) {
+        u16x2 m = {0, 0};
+#pragma unroll
+        for (int k = 0; k < 32; ++k) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[k].w[0] & 0x7fff7fffu));
+        ea = scale_byte((uint32_t)m[0] >> 7);
+        eb = scale_byte((uint32_t)m[1] >> 7);
+        const float sa = scale_of(ea), sb = scale_of(eb);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            uint32_t p = 0, q = 0;
+#define DOBB_MX4_PAIR(k)                                                                                             \
+            p = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(                                                            \
+                p, __builtin_bit_cast(bf16x2, __builtin_amdgcn_perm(v[8 * w + 2 * k + 1].w[0], v[8 * w + 2 * k].w[0], 0x05040100u)), sa, k); \
+            q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(                                                            \
+                q, __builtin_bit_cast(bf16x2, __builtin_amdgcn_perm(v[8 * w + 2 * k + 1].w[0], v[8 * w + 2 * k].w[0], 0x07060302u)), sb, k);
+            DOBB_MX4_PAIR(0) DOBB_MX4_PAIR(1) DOBB_MX4_PAIR(2) DOBB_MX4_PAIR(3)
+#undef DOBB_MX4_PAIR
+            qa[w] = p;
+            qb[w] = q;
+        }
+    } else {
+        uint32_t ma = 0, mb = 0;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+            ma = max(ma, v[k].w[0] & 0x7fffffffu);
+            mb = max(mb, v[k].w[BF16 ? 0 : 1] & 0x7fffffffu);
+        }
+        ea = scale_byte(ma >> 23);
+        eb = scale_byte(mb >> 23);
+        const float sa = scale_of(ea), sb = scale_of(eb);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            uint32_t p = 0, q = 0;
+#define DOBB_MX4_AT(t, c) __uint_as_float(v[8 * w + (t)].w[BF16 ? 0 : (c)])
+#define DOBB_MX4_PAIR(k)                                                                                             \
+            p = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(p, DOBB_MX4_AT(2 * k, 0), DOBB_MX4_AT(2 * k + 1, 0), sa, k);  \
+            q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, DOBB_MX4_AT(2 * k, 1), DOBB_MX4_AT(2 * k + 1, 1), sb, k);
+            DOBB_MX4_PAIR(0) DOBB_MX4_PAIR(1) DOBB_MX4_PAIR(2) DOBB_MX4_PAIR(3)
+#undef DOBB_MX4_PAIR
+#undef DOBB_MX4_AT
+            qa[w] = p;
+            qb[w] = q;
+        }
+    }
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {                           // a group that is not finite holds zeros
+        if (ea == 255) qa[w] = 0;
+        if (eb == 255) qb[w] = 0;
+    }
+}
 
 template <bool BF16>
 __global__ void __launch_bounds__(256) k_mx4_quantize(int64_t N, int64_t n, int64_t ldx, unsigned colblocks, const void *X,
@@ -34,72 +96,34 @@ __global__ void __launch_bounds__(256) k_mx4_quantize(int64_t N, int64_t n, int6
     // last token repeat it and become zeros below, a pair past the last column moves to the last two.
     constexpr int ES = BF16 ? 2 : 4;
     const uint32_t xc = (uint32_t)(c + 1 < n ? c : n > 1 ? n - 2 : 0) * ES;
-    const char *x = (const char *)X + (t0 < N ? t0 : 0) * ldx * ES;   // the same for the wave: rows by scalar address
-    float a[32], b[32];
-    if (rows == 0) {
+    const char *x = (const char *)X + (t0 < N ? t0 : 0) * ldx * ES;
+    const int last = rows > 0 ? rows - 1 : 0;
+    Pair<BF16> v[32];
+    if (n > 1) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) a[k] = b[k] = 0.f;
+        for (int k = 0; k < 32; ++k) v[k] = *(const Pair<BF16> *)(x + min(k, last) * ldx * ES + xc);
     } else {
-        Pair<BF16> v[32];
-        if (n > 1) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = *(const Pair<BF16> *)(x + min(k, rows - 1) * ldx * ES + xc);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-                const char *r = x + min(k, rows - 1) * ldx * ES + xc;
-                v[k].w[0] = BF16 ? *(const uint16_t *)r : *(const uint32_t *)r;
-                if (!BF16) v[k].w[BF16 ? 0 : 1] = 0;
-            }
-        }
-        const bool last = n > 1 && c + 1 >= n;              // the pair's second column is this lane's first
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
-            a[k] = BF16 ? __uint_as_float(v[k].w[0] << 16) : __uint_as_float(v[k].w[0]);
-            b[k] = BF16 ? __uint_as_float(v[k].w[0] & 0xffff0000u) : __uint_as_float(v[k].w[BF16 ? 0 : 1]);
+            const char *r = x + min(k, last) * ldx * ES + xc;
+            v[k].w[0] = BF16 ? *(const uint16_t *)r : *(const uint32_t *)r;
+            if (!BF16) v[k].w[BF16 ? 0 : 1] = 0;
         }
-        if (last)
-#pragma unroll
-            for (int k = 0; k < 32; ++k) a[k] = b[k];
-        if (rows < 32)
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-                a[k] = k < rows ? a[k] : 0.f;
-                b[k] = k < rows ? b[k] : 0.f;
-            }
     }
-    uint32_t ma = 0, mb = 0;
+    if (n > 1 && c + 1 >= n)                                // the pair's second column is this lane's first
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
-        ma = max(ma, mag(a[k]));
-        mb = max(mb, mag(b[k]));
-    }
-    uint32_t ea = ma >> 23, eb = mb >> 23;                     // exponent + 127; the scale is two below it
-    const bool na = ea == 255, nb = eb == 255;
-    ea = ea < 2 ? 0 : ea - 2;
-    eb = eb < 2 ? 0 : eb - 2;
-    const float sa = __uint_as_float(ea << 23), sb = __uint_as_float(eb << 23);   // 0 stands for 2^-127
-    uint32_t qa[4], qb[4];
+        for (int k = 0; k < 32; ++k) v[k].w[0] = BF16 ? v[k].w[0] >> 16 : v[k].w[BF16 ? 0 : 1];
+    if (rows < 32)
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        uint32_t p = 0, q = 0;
-        const int k = 8 * w;
-        p = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(p, a[k], a[k + 1], sa, 0);
-        p = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(p, a[k + 2], a[k + 3], sa, 1);
-        p = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(p, a[k + 4], a[k + 5], sa, 2);
-        p = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(p, a[k + 6], a[k + 7], sa, 3);
-        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, b[k], b[k + 1], sb, 0);
-        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, b[k + 2], b[k + 3], sb, 1);
-        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, b[k + 4], b[k + 5], sb, 2);
-        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, b[k + 6], b[k + 7], sb, 3);
-        qa[w] = na ? 0u : p;
-        qb[w] = nb ? 0u : q;
-    }
+        for (int k = 0; k < 32; ++k)
+            if (k >= rows) v[k].w[0] = v[k].w[BF16 ? 0 : 1] = 0;
+    uint32_t qa[4], qb[4], ea, eb;
+    quantize_pair<BF16>(v, ea, eb, qa, qb);
     uint4 *o = codes + (tile * 4 + g) * n + c;
     if (c < n) o[0] = uint4{qa[0], qa[1], qa[2], qa[3]};
     if (c + 1 < n) o[1] = uint4{qb[0], qb[1], qb[2], qb[3]};
-    sc[2 * lane][g] = (uint8_t)(na ? 255u : ea);
-    sc[2 * lane + 1][g] = (uint8_t)(nb ? 255u : eb);
+    sc[2 * lane][g] = (uint8_t)ea;
+    sc[2 * lane + 1][g] = (uint8_t)eb;
     __syncthreads();
     if (threadIdx.x < kCols && c0 + threadIdx.x < n) scales[tile * n + c0 + threadIdx.x] = *(const uint32_t *)sc[threadIdx.x];
 }
@@ -121,8 +145,7 @@ __global__ void __launch_bounds__(256) k_mx4_dequantize(int64_t N, int64_t n, in
     const uint4 ca = p[0], cb = two ? p[1] : uint4{0, 0, 0, 0};
     const uint8_t *s = scales + (tile * n + c) * 4 + g;
     const uint32_t ea = s[0], eb = two ? s[4] : 0;
-    // the scale's float has e as its exponent field (0: 2^-127); 255 reads back as NaN
-    const float sa = __uint_as_float(ea << 23), sb = __uint_as_float(eb << 23);
+    const float sa = scale_of(ea), sb = scale_of(eb);
     const uint32_t wa[4] = {ca.x, ca.y, ca.z, ca.w}, wb[4] = {cb.x, cb.y, cb.z, cb.w};
     constexpr int ES = BF16 ? 2 : 4;
     char *o = (char *)out + t0 * ldo * ES;
