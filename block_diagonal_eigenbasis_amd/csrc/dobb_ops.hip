@@ -40,6 +40,21 @@ dobb_status check_list(int count, const int64_t *numel, const void *const *p, co
 // Every buffer written is the tensor it is made from (same type) or apart from everything else in the
 // list: a chunk of one is then read and written by one workgroup only.
 dobb_status check_outputs(const GradArgs &a) {
+    // Most lists are laid out in order, the tensors written apart from those read or the very same: seen in
+    // one pass, without sorting
+    bool ordered = true, same = true;
+    uintptr_t end = 0, out_lo = UINTPTR_MAX, in_lo = UINTPTR_MAX, in_hi = 0;
+    for (int i = 0; i < a.count; ++i) {
+        if (a.numel[i] == 0) continue;
+        const uintptr_t g = (uintptr_t)a.G[i], o = (uintptr_t)a.out[i];
+        same = same && g == o && a.g_dtypes[i] == a.out_dtypes[i];
+        ordered = ordered && o >= end;
+        end = o + (uintptr_t)(a.numel[i] * size_of(a.out_dtypes[i]));
+        out_lo = std::min(out_lo, o);
+        in_lo = std::min(in_lo, g);
+        in_hi = std::max(in_hi, g + (uintptr_t)(a.numel[i] * size_of(a.g_dtypes[i])));
+    }
+    if (ordered && (same || in_hi <= out_lo || end <= in_lo)) return DOBB_OK;
     struct Span {
         uintptr_t lo, hi;
         bool out;

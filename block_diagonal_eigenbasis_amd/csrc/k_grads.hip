@@ -14,6 +14,7 @@ namespace {
 
 constexpr int kNormMats = 192;   // tensors per launch: the tables fit the 4 KB of kernel arguments
 constexpr int kClipMats = 128;
+constexpr int kFinishMats = 900;
 constexpr int kUnroll = 4;       // 16-byte vectors in flight per thread
 constexpr int kThreads = 256;
 constexpr int64_t kStep = (int64_t)kThreads * kUnroll;   // vectors a workgroup reads at a time
@@ -23,6 +24,10 @@ struct NormTable {
     int64_t numel[kNormMats];
     uint32_t first[kNormMats + 1];          // first chunk of each tensor, counted from this launch's
     uint32_t bf16[(kNormMats + 31) / 32];
+};
+
+struct FinishTable {
+    uint32_t first[kFinishMats + 1];        // counted from the first table's
 };
 
 struct ClipTable {
@@ -36,13 +41,21 @@ struct ClipTable {
 // 16 bytes at the alignment of one entry
 struct __attribute__((packed, aligned(2))) Vec16 { uint32_t w[4]; };
 
+// the tensor of a chunk: how many of the ascending first[0 .. cnt - 1] are at most chunk, less one.  One
+// read a lane and a ballot for every 64 (bisecting was a chain of eight dependent reads)
+template <int MATS>
 __device__ __forceinline__ int find_tensor(const uint32_t *first, int cnt, uint32_t chunk) {
-    int lo = 0, hi = cnt;                    // first[lo] <= chunk < first[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (first[mid] <= chunk) lo = mid; else hi = mid;
+    const int lane = threadIdx.x & 63;
+    bool le[(MATS + 63) / 64];
+#pragma unroll
+    for (int k = 0; k < (MATS + 63) / 64; ++k) {
+        const int i = 64 * k + lane;
+        le[k] = first[i < MATS ? i : MATS] <= chunk && i < cnt;
     }
-    return lo;
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < (MATS + 63) / 64; ++k) n += __popcll(__ballot(le[k]));
+    return __builtin_amdgcn_readfirstlane(n - 1);
 }
 
 __device__ __forceinline__ double sq(float v) { return (double)v * (double)v; }
@@ -56,21 +69,34 @@ __device__ __forceinline__ double sumsq_chunk(const char *g, int64_t numel, int6
     const int64_t whole = numel / E;                    // vectors that lie inside the tensor
     const int64_t end = v0 + nv < whole ? v0 + nv : whole;
     double s0 = 0.0, s1 = 0.0;
-    for (int64_t v = v0 + threadIdx.x; v < end; v += kStep) {
+    auto add = [&](const Vec16 &x) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (BF16) { s0 += sq(lo_bf16(x.w[c])); s1 += sq(hi_bf16(x.w[c])); }
+            else if (c & 1) s1 += sq(__uint_as_float(x.w[c]));
+            else s0 += sq(__uint_as_float(x.w[c]));
+        }
+    };
+    int64_t b = v0;
+    for (; b + kStep <= end; b += kStep) {              // whole steps: no bounds to check
         Vec16 x[kUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int64_t p = v + u * kThreads;
-            x[u] = p < end ? *(const Vec16 *)(g + p * 16) : Vec16{{0, 0, 0, 0}};
+        for (int u = 0; u < kUnroll; ++u) x[u] = *(const Vec16 *)(g + (b + u * kThreads + threadIdx.x) * 16);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) add(x[u]);
+    }
+    if (b < end) {
+        Vec16 x[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {             // places past the end repeat the last vector
+            const int64_t p = b + u * kThreads + threadIdx.x;
+            x[u] = *(const Vec16 *)(g + (p < end ? p : end - 1) * 16);
         }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if (BF16) { s0 += sq(lo_bf16(x[u].w[c])); s1 += sq(hi_bf16(x[u].w[c])); }
-                else if (c & 1) s1 += sq(__uint_as_float(x[u].w[c]));
-                else s0 += sq(__uint_as_float(x[u].w[c]));
-            }
+            if (b + u * kThreads + threadIdx.x < end) add(x[u]);
     }
     if (whole >= v0 && whole < v0 + nv) {               // the entries behind the last whole vector
         const int64_t e = whole * E + threadIdx.x;
@@ -95,7 +121,7 @@ __device__ __forceinline__ double block_sum(double s, double *sm) {
 __global__ void __launch_bounds__(kThreads) k_grad_sumsq(int cnt, int64_t nv, double *part, NormTable t) {
     __shared__ double sm[kThreads / 64];
     const uint32_t chunk = blockIdx.x;
-    const int i = find_tensor(t.first, cnt, chunk);
+    const int i = find_tensor<kNormMats>(t.first, cnt, chunk);
     const int64_t v0 = (int64_t)(chunk - t.first[i]) * nv;
     const bool bf = (t.bf16[i >> 5] >> (i & 31)) & 1;
     const double s = block_sum(bf ? sumsq_chunk<true>((const char *)t.g[i], t.numel[i], v0, nv)
@@ -103,16 +129,26 @@ __global__ void __launch_bounds__(kThreads) k_grad_sumsq(int cnt, int64_t nv, do
     if (threadIdx.x == 0) part[chunk] = s;
 }
 
-// workgroup i < cnt: norms[i] from its tensor's chunks; workgroup cnt (when total is asked for): the
-// norm of all `all` chunks of the call, which start at part0
-__global__ void __launch_bounds__(1024) k_grad_norms(int cnt, const double *part, const double *part0, uint32_t all,
-                                                     float *norms, float *total, NormTable t) {
-    __shared__ double sm[16];
+// workgroup i < cnt: norms[i] from its tensor's chunks of part; workgroup cnt (where there is one): the
+// norm of all `all` chunks of the call
+__global__ void __launch_bounds__(512) k_grad_norms(int cnt, const double *part, uint32_t all, float *norms, float *total,
+                                                    FinishTable t) {
+    __shared__ double sm[8];
     const int i = blockIdx.x;
-    const double *p = i < cnt ? part + t.first[i] : part0;
-    const uint32_t len = i < cnt ? t.first[i + 1] - t.first[i] : all;
+    const uint32_t k0 = i < cnt ? t.first[i] : 0, k1 = i < cnt ? t.first[i + 1] : all;
     double s = 0.0;
-    for (uint32_t k = threadIdx.x; k < len; k += 1024) s += p[k];
+    for (uint32_t b = k0; b < k1; b += 8 * 512) {
+        double x[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const uint32_t k = b + u * 512 + threadIdx.x;
+            x[u] = part[k < k1 ? k : k1 - 1];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (b + u * 512 + threadIdx.x < k1) s += x[u];
+    }
     s = block_sum(s, sm);
     if (threadIdx.x == 0) *(i < cnt ? norms + i : total) = (float)sqrt(s);
 }
@@ -128,27 +164,39 @@ __device__ __forceinline__ void scale_chunk(const char *g, char *o, int64_t nume
     constexpr int OB = E * (OBF ? 2 : 4);
     const int64_t whole = numel / E;
     const int64_t end = v0 + nv < whole ? v0 + nv : whole;
-    for (int64_t v = v0 + threadIdx.x; v < end; v += kStep) {
+    auto put = [&](int64_t p, const Vec16 &x) {
+        float f[E];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (IBF) { f[2 * k] = lo_bf16(x.w[k]) * c; f[2 * k + 1] = hi_bf16(x.w[k]) * c; }
+            else f[k] = __uint_as_float(x.w[k]) * c;
+        }
+        struct __attribute__((packed, aligned(2))) Out { uint32_t w[OB / 4]; } r;
+#pragma unroll
+        for (int k = 0; k < OB / 4; ++k) r.w[k] = OBF ? pack_bf16(f[2 * k], f[2 * k + 1]) : __float_as_uint(f[k]);
+        *(Out *)(o + p * OB) = r;
+    };
+    int64_t b = v0;
+    for (; b + kStep <= end; b += kStep) {              // whole steps: no bounds to check
         Vec16 x[kUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int64_t p = v + u * kThreads;
-            if (p < end) x[u] = *(const Vec16 *)(g + p * 16);
+        for (int u = 0; u < kUnroll; ++u) x[u] = *(const Vec16 *)(g + (b + u * kThreads + threadIdx.x) * 16);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) put(b + u * kThreads + threadIdx.x, x[u]);
+    }
+    if (b < end) {
+        Vec16 x[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {             // places past the end read the last vector, for nothing
+            const int64_t p = b + u * kThreads + threadIdx.x;
+            x[u] = *(const Vec16 *)(g + (p < end ? p : end - 1) * 16);
         }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int64_t p = v + u * kThreads;
-            if (p >= end) break;
-            float f[E];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (IBF) { f[2 * k] = lo_bf16(x[u].w[k]) * c; f[2 * k + 1] = hi_bf16(x[u].w[k]) * c; }
-                else f[k] = __uint_as_float(x[u].w[k]) * c;
-            }
-            struct __attribute__((packed, aligned(2))) Out { uint32_t w[OB / 4]; } r;
-#pragma unroll
-            for (int k = 0; k < OB / 4; ++k) r.w[k] = OBF ? pack_bf16(f[2 * k], f[2 * k + 1]) : __float_as_uint(f[k]);
-            *(Out *)(o + p * OB) = r;
+            const int64_t p = b + u * kThreads + threadIdx.x;
+            if (p < end) put(p, x[u]);
         }
     }
     if (whole >= v0 && whole < v0 + nv) {
@@ -165,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) k_grad_clip(int cnt, int64_t nv, con
     const float q = max_norm / (*total + 1e-6f);
     const float c = q > 1.f ? 1.f : q;                 // a NaN stays one
     const uint32_t chunk = blockIdx.x;
-    const int i = find_tensor(t.first, cnt, chunk);
+    const int i = find_tensor<kClipMats>(t.first, cnt, chunk);
     const char *g = (const char *)t.g[i];
     char *o = (char *)t.out[i];
     if (c == 1.f && (const char *)o == g) return;
@@ -183,7 +231,6 @@ int64_t vectors(int64_t numel, dobb_dtype dt) {
 }
 
 constexpr int64_t kMostChunks = 8192;
-constexpr int64_t kClipChunk = 4 * kStep;
 
 }  // namespace
 
@@ -205,6 +252,10 @@ int64_t grad_norm_chunks(int count, const int64_t *numel, const dobb_dtype *dt) 
 
 hipError_t launch_grad_norm(const GradArgs &a, float *norms, float *total, double *part, hipStream_t s) {
     const int64_t nv = grad_norm_chunk(a.count, a.numel, a.g_dtypes);
+    auto chunks_of = [&](int i) { return (vectors(a.numel[i], a.g_dtypes[i]) + nv - 1) / nv; };
+    int64_t all = 0;
+    for (int i = 0; i < a.count; ++i) all += chunks_of(i);
+    if (all > 0x7fffffff) return hipErrorInvalidValue;
     double *p = part;
     for (int i0 = 0; i0 < a.count; i0 += kNormMats) {
         const int cnt = a.count - i0 < kNormMats ? a.count - i0 : kNormMats;
@@ -214,47 +265,59 @@ hipError_t launch_grad_norm(const GradArgs &a, float *norms, float *total, doubl
             t.g[i] = a.G[i0 + i];
             t.numel[i] = a.numel[i0 + i];
             t.first[i] = (uint32_t)chunks;
-            chunks += (vectors(t.numel[i], a.g_dtypes[i0 + i]) + nv - 1) / nv;
+            chunks += chunks_of(i0 + i);
             if (a.g_dtypes[i0 + i] == DOBB_BF16) t.bf16[i >> 5] |= 1u << (i & 31);
         }
-        t.first[cnt] = (uint32_t)chunks;
-        if (chunks > 0x7fffffff) return hipErrorInvalidValue;
-        if (chunks > 0)
-            DOBB_LAUNCH("grad_sumsq", s, k_grad_sumsq, dim3((unsigned)chunks), dim3(kThreads), 0, cnt, nv, p, t);
-        const bool last = i0 + cnt == a.count;
-        const int nn = norms ? cnt : 0;
-        if (nn + (last ? 1 : 0) > 0)
-            DOBB_LAUNCH("grad_norms", s, k_grad_norms, dim3((unsigned)(nn + (last ? 1 : 0))), dim3(1024), 0, nn, p, part,
-                        (uint32_t)(p - part + chunks), norms ? norms + i0 : nullptr, total, t);
+        if (chunks == 0) continue;
+        DOBB_LAUNCH("grad_sumsq", s, k_grad_sumsq, dim3((unsigned)chunks), dim3(kThreads), 0, cnt, nv, p, t);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         p += chunks;
+    }
+    int64_t at = 0;
+    for (int i0 = 0; i0 < a.count; i0 += kFinishMats) {
+        const int cnt = a.count - i0 < kFinishMats ? a.count - i0 : kFinishMats;
+        const bool last = i0 + cnt == a.count;
+        if (!norms && !last) continue;
+        FinishTable t{};
+        if (norms) {
+            for (int i = 0; i < cnt; ++i) { t.first[i] = (uint32_t)at; at += chunks_of(i0 + i); }
+            t.first[cnt] = (uint32_t)at;
+        }
+        const int nn = norms ? cnt : 0;
+        DOBB_LAUNCH("grad_norms", s, k_grad_norms, dim3((unsigned)(nn + (last ? 1 : 0))), dim3(512), 0, nn, part, (uint32_t)all,
+                    norms ? norms + i0 : nullptr, total, t);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
     }
     return hipSuccess;
 }
 
 hipError_t launch_grad_clip(const GradArgs &a, const float *total, float max_norm, hipStream_t s) {
+    // vectors per workgroup: one step where that gives no more workgroups than run at once, up to four
+    int64_t all = 0;
+    for (int i = 0; i < a.count; ++i) all += vectors(a.numel[i], a.g_dtypes[i]);
+    const int64_t steps = all / (kStep * 2048);
+    const int64_t nv = (steps < 1 ? 1 : steps > 4 ? 4 : steps) * kStep;
     for (int i0 = 0; i0 < a.count;) {
         ClipTable t{};
         int64_t chunks = 0;
         int cnt = 0;
         for (; i0 + cnt < a.count && cnt < kClipMats; ++cnt) {
             const int i = i0 + cnt;
+            const int64_t c = (vectors(a.numel[i], a.g_dtypes[i]) + nv - 1) / nv;
+            if (chunks + c > 0x7fffffff) break;
             t.g[cnt] = a.G[i];
             t.out[cnt] = a.out[i];
             t.numel[cnt] = a.numel[i];
             t.first[cnt] = (uint32_t)chunks;
-            const int64_t c = (vectors(a.numel[i], a.g_dtypes[i]) + kClipChunk - 1) / kClipChunk;
-            if (cnt > 0 && chunks + c > 0x7fffffff) break;
             chunks += c;
             if (a.g_dtypes[i] == DOBB_BF16) t.bf16[cnt >> 5] |= 1u << (cnt & 31);
             if (a.out_dtypes[i] == DOBB_BF16) t.out_bf16[cnt >> 5] |= 1u << (cnt & 31);
         }
-        if (chunks > 0x7fffffff) return hipErrorInvalidValue;
-        t.first[cnt] = (uint32_t)chunks;
+        if (cnt == 0) return hipErrorInvalidValue;
         if (chunks > 0)
-            DOBB_LAUNCH("grad_clip", s, k_grad_clip, dim3((unsigned)chunks), dim3(kThreads), 0, cnt, kClipChunk, total,
-                        max_norm, t);
+            DOBB_LAUNCH("grad_clip", s, k_grad_clip, dim3((unsigned)chunks), dim3(kThreads), 0, cnt, nv, total, max_norm, t);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         i0 += cnt;

@@ -128,8 +128,8 @@ __device__ __forceinline__ Place place(int whole, int nsplit, int nwg) {
     return p;
 }
 
-// F = ceil(nb / 32) fragments
-template <int F>
+// F = ceil(nb / 32) fragments; NT: the codes are read past the caches
+template <int F, bool NT>
 __global__ void __launch_bounds__(256, 2) k_moment_mx4_narrow(int cnt, int nb, int64_t tiles, int whole, int nsplit_, double beta,
                                                               double scale, float *partial, MomentTable t) {
     constexpr int PAIRS = F * (F + 1) / 2;
@@ -176,7 +176,10 @@ __global__ void __launch_bounds__(256, 2) k_moment_mx4_narrow(int cnt, int nb, i
     auto load_group = [&](int g) {
         const char *gp = cp + g * (16 * n);
 #pragma unroll
-        for (int f = 0; f < F; ++f) a[g][f] = *(const i32x4 *)(gp + (mine + 4 * ci[f]));
+        for (int f = 0; f < F; ++f) {
+            const i32x4 *x = (const i32x4 *)(gp + (mine + 4 * ci[f]));
+            a[g][f] = NT ? __builtin_nontemporal_load(x) : *x;
+        }
     };
     auto take_scales = [&]() {
 #pragma unroll
@@ -524,13 +527,23 @@ hipError_t launch_moment_mx4(const MomentMx4Args &a, hipStream_t s) {
     const double scale = (1.0 - (double)a.beta) / (double)a.N;
     const unsigned grid = (unsigned)wgs;
     hipError_t e = hipSuccess;
-#define DOBB_MX4_NARROW(F)                                                                                             \
-    DOBB_LAUNCH("moment_mx4_narrow", s, k_moment_mx4_narrow<F>, dim3(grid), dim3(256), 0, a.count, nb, a.tiles, a.plan.whole, \
-                a.plan.nsplit, (double)a.beta, scale, a.partial, t)
+    // Captures larger than half of the 256 MB cache behind the L2s are read past it: what the quantising
+    // left there is gone by then (36 weights of 1600 columns, 16384 tokens, 501 MB: 124 -> 112 us); a smaller
+    // set may still be there (a 7B-style layer, 4096 tokens, 77 MB: 33 us from the cache, 36 past it).
+    const bool nt = blocks * a.nb * a.tiles * 68 > ((int64_t)128 << 20);
+#define DOBB_MX4_NARROW_(F, NT)                                                                                       \
+    DOBB_LAUNCH("moment_mx4_narrow", s, (k_moment_mx4_narrow<F, NT>), dim3(grid), dim3(256), 0, a.count, nb, a.tiles,    \
+                a.plan.whole, a.plan.nsplit, (double)a.beta, scale, a.partial, t)
+#define DOBB_MX4_NARROW(F)                     \
+    do {                                       \
+        if (nt) DOBB_MX4_NARROW_(F, true);     \
+        else DOBB_MX4_NARROW_(F, false);       \
+    } while (0)
     if (F == 1) DOBB_MX4_NARROW(1);
     else if (F == 2) DOBB_MX4_NARROW(2);
     else if (F == 3) DOBB_MX4_NARROW(3);
     else if (F == 4) DOBB_MX4_NARROW(4);
+#undef DOBB_MX4_NARROW_
 #undef DOBB_MX4_NARROW
     else if (F <= 8) e = launch_wide<4, 4, 1>(a, t, grid, F, nwg, scale, s);
     else if (F <= 12) e = launch_wide<4, 6, 2>(a, t, grid, F, nwg, scale, s);

@@ -14,6 +14,7 @@ namespace {
 
 constexpr int kCols = 128;   // columns per workgroup
 
+typedef uint32_t __attribute__((aligned(2))) packed_u32;
 template <bool BF16>
 struct __attribute__((packed, aligned(2))) Pair { uint32_t w[BF16 ? 1 : 2]; };
 
@@ -101,7 +102,11 @@ __global__ void __launch_bounds__(256) k_mx4_quantize(int64_t N, int64_t n, int6
     Pair<BF16> v[32];
     if (n > 1) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] = *(const Pair<BF16> *)(x + min(k, last) * ldx * ES + xc);
+        for (int k = 0; k < 32; ++k) {                      // read once: past the caches (16384 x 6400 in bf16:
+            const uint32_t *r = (const uint32_t *)(x + min(k, last) * ldx * ES + xc);   // 62 -> 49 us)
+            v[k].w[0] = __builtin_nontemporal_load((const packed_u32 *)r);
+            if (!BF16) v[k].w[BF16 ? 0 : 1] = __builtin_nontemporal_load((const packed_u32 *)r + 1);
+        }
     } else {
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
