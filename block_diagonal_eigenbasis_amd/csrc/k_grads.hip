@@ -226,8 +226,8 @@ __global__ void __launch_bounds__(kThreads) k_grad_clip(int cnt, int64_t nv, con
 }
 
 int64_t vectors(int64_t numel, dobb_dtype dt) {
-    const int e = dt == DOBB_BF16 ? 8 : 4;
-    return numel / e + (numel % e != 0);
+    const int sh = dt == DOBB_BF16 ? 3 : 2;
+    return (numel + (1 << sh) - 1) >> sh;
 }
 
 constexpr int64_t kMostChunks = 8192;

@@ -67,45 +67,57 @@ __device__ __forceinline__ f32x16 mfma_fp4(const i32x4 &a, const i32x4 &b, f32x1
 __device__ __forceinline__ void batch() { __builtin_amdgcn_sched_barrier(0); }
 
 constexpr int kPairPad = 33;                   // row pitch of a 32x32 pair in LDS: rows and columns are read
-typedef float PairTile[32][kPairPad];
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 
-// One wave: a finished 32 x 32 pair at rows i0 and columns j0 of a block, from its LDS tile.  A split's
-// partial sums leave as rows of the lower triangle; a whole sum becomes the new entries of A, rows of
-// the lower triangle and, read from the tile by columns, of the upper one.  The entries of A are read in
-// one batch, at clamped places rather than under a condition.
-__device__ __forceinline__ void store_pair(float *out, int nb, int i0, int j0, PairTile &tile, bool part, double beta, double scale) {
-    const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
-    float av[16];
-    if (!part && beta > 0.0) {
+// One wave: a finished 32 x 32 pair at rows i0 and columns j0 of a block, in the accumulators' layout.
+// read_pair takes its old entries of A; store_pair writes a split's partial sums as rows of the lower
+// triangle, or the new entries of A as rows of the lower triangle and of the upper one, straight from the
+// registers: a lane's four consecutive rows are 16 contiguous bytes of the mirrored row.  A load that
+// follows a store waits for it (both count in order), so callers read for several pairs before they store
+// the first: pair by pair, an exchange with memory each, the stores were most of a short call.
+// (a block has at most 2^20 entries: 32-bit offsets from a scalar address)
+__device__ __forceinline__ float *at(const float *base, int e) { return (float *)((char *)base + (uint32_t)e * 4u); }
+
+__device__ __forceinline__ void read_pair(const float *out, int nb, int i0, int j0, float (&av)[16]) {
+    const int lane = threadIdx.x & 63;
 #pragma unroll
-        for (int u = 0; u < 16; ++u) {
-            const int i = min(i0 + 2 * u + half, nb - 1), j = min(j0 + col, i);
-            av[u] = out[(int64_t)i * nb + j];
-        }
+    for (int r = 0; r < 16; ++r) {
+        const int i = min(i0 + acc_row(r, lane), nb - 1), j = min(j0 + (lane & 31), i);   // no branches
+        av[r] = *at(out, i * nb + j);
+    }
+}
+
+__device__ __forceinline__ void store_pair(float *out, int nb, int i0, int j0, const f32x16 &sum, const float (&av)[16], bool part,
+                                           double beta, double scale) {
+    const int lane = threadIdx.x & 63, j = j0 + (lane & 31);
+    const bool inside = i0 + 32 <= nb && j0 < i0;                     // no bounds needed
+    const int low = i0 * nb + j;                                      // + acc_row * nb: the pair's entries
+    const int up = j * nb + i0 + 4 * (lane >> 5);                     // + 8 k: their mirrored ones, by fours
+    if (part) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            if (inside || (i0 + acc_row(r, lane) < nb && j <= i0 + acc_row(r, lane))) *at(out, low + acc_row(r, lane) * nb) = sum[r];
+        return;
     }
     float w[16];
 #pragma unroll
-    for (int u = 0; u < 16; ++u) w[u] = tile[2 * u + half][col];
-    batch();
-    if (!part)
+    for (int r = 0; r < 16; ++r) w[r] = moment_out(beta, scale, av[r], (double)sum[r]);
+    if (inside) {
 #pragma unroll
-        for (int u = 0; u < 16; ++u) w[u] = moment_out(beta, scale, av[u], (double)w[u]);
+        for (int r = 0; r < 16; ++r) *at(out, low + acc_row(r, lane) * nb) = w[r];
 #pragma unroll
-    for (int u = 0; u < 16; ++u) {
-        const int i = i0 + 2 * u + half, j = j0 + col;
-        if (i < nb && j <= i) out[(int64_t)i * nb + j] = w[u];
+        for (int k = 0; k < 4; ++k) *(f32x4u *)at(out, up + 8 * k) = f32x4u{w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]};
+        return;
     }
-    if (part) return;
 #pragma unroll
-    for (int u = 0; u < 16; ++u) tile[2 * u + half][col] = w[u];
-    __builtin_amdgcn_wave_barrier();
+    for (int r = 0; r < 16; ++r) {
+        const int i = i0 + acc_row(r, lane);
+        if (i < nb && j <= i) *at(out, low + acc_row(r, lane) * nb) = w[r];
+    }
 #pragma unroll
-    for (int u = 0; u < 16; ++u) w[u] = tile[col][2 * u + half];
-    batch();
-#pragma unroll
-    for (int u = 0; u < 16; ++u) {
-        const int i = i0 + col, j = j0 + 2 * u + half;
-        if (i < nb && j < i) out[(int64_t)j * nb + i] = w[u];
+    for (int r = 0; r < 16; ++r) {
+        const int i = i0 + acc_row(r, lane);
+        if (i < nb && j < i) *at(out, up + 8 * (r >> 2) + (r & 3)) = w[r];
     }
 }
 
@@ -134,7 +146,7 @@ __global__ void __launch_bounds__(256, 2) k_moment_mx4_narrow(int cnt, int nb, i
                                                               double scale, float *partial, MomentTable t) {
     constexpr int PAIRS = F * (F + 1) / 2;
     constexpr int PH = PAIRS > 6 ? 5 : PAIRS;   // pairs that are added up at a time
-    __shared__ PairTile sm[PH][3];
+    __shared__ f32x4 sm[PH][3][4][64];          // accumulators on their way from wave to wave, lane to lane
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 31, half = lane >> 5;
     const Place pl = place(whole, nsplit_, 1);
@@ -216,6 +228,17 @@ __global__ void __launch_bounds__(256, 2) k_moment_mx4_narrow(int cnt, int nb, i
     const int64_t nbb = (int64_t)nb * nb;
     const bool part = pl.nsplit > 1;
     float *out = part ? partial + ((int64_t)(blk - whole) * pl.nsplit + pl.split) * nbb : t.A[mat] + (blk - t.first[mat]) * nbb;
+    constexpr int OWN = (PAIRS + 3) / 4;        // pairs wave, wave + 4, ..
+    int fi[OWN], fj[OWN];
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {
+        fi[o] = 0;
+        fj[o] = 4 * o + wave;
+        while (fj[o] > fi[o]) fj[o] -= ++fi[o];
+    }
+    const bool old = !part && beta > 0.0;
+    float av[2][16];
+    f32x16 own[OWN];
 #pragma unroll
     for (int h = 0; h < PAIRS; h += PH) {
         if (h > 0) __syncthreads();
@@ -223,26 +246,29 @@ __global__ void __launch_bounds__(256, 2) k_moment_mx4_narrow(int cnt, int nb, i
         for (int p = h; p < h + PH && p < PAIRS; ++p)
             if (wave != p % 4)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) sm[p - h][(wave + 3 - p) & 3][acc_row(r, lane)][col] = acc[p][r];
+                for (int k = 0; k < 4; ++k)
+                    sm[p - h][(wave + 3 - p) & 3][k][lane] = f32x4{acc[p][4 * k], acc[p][4 * k + 1], acc[p][4 * k + 2], acc[p][4 * k + 3]};
         __syncthreads();
 #pragma unroll
         for (int p = h; p < h + PH && p < PAIRS; ++p)
             if (wave == p % 4) {
-                float x[3][16];
+                f32x4 x[3][4];
 #pragma unroll
-                for (int k = 0; k < 3; ++k)
+                for (int s = 0; s < 3; ++s)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) x[k][r] = sm[p - h][k][acc_row(r, lane)][col];
-                batch();
+                    for (int k = 0; k < 4; ++k) x[s][k] = sm[p - h][s][k][lane];
 #pragma unroll
-                for (int r = 0; r < 16; ++r) sm[p - h][0][acc_row(r, lane)][col] = ((acc[p][r] + x[0][r]) + x[1][r]) + x[2][r];
+                for (int r = 0; r < 16; ++r)
+                    own[p / 4][r] = ((acc[p][r] + x[0][r >> 2][r & 3]) + x[1][r >> 2][r & 3]) + x[2][r >> 2][r & 3];
             }
-        int fi = 0, fj = 0;
-#pragma unroll 1
-        for (int p = 0; p < h + PH && p < PAIRS; ++p) {
-            if (p >= h && wave == p % 4) store_pair(out, nb, 32 * fi, 32 * fj, sm[p - h][0], part, beta, scale);
-            if (++fj > fi) { fj = 0; ++fi; }
-        }
+    }
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {             // the old entries of the next pair read before the stores of this one
+        if (old && o == 0) read_pair(out, nb, 32 * fi[0], 32 * fj[0], av[0]);
+        if (old && o + 1 < OWN) read_pair(out, nb, 32 * fi[o + 1], 32 * fj[o + 1], av[(o + 1) & 1]);
+        batch();
+        if (4 * o + wave < PAIRS) store_pair(out, nb, 32 * fi[o], 32 * fj[o], own[o], av[o & 1], part, beta, scale);
+        batch();
     }
 }
 
@@ -375,32 +401,42 @@ __global__ void __launch_bounds__(kWideThreads, 2) k_moment_mx4_wide(int cnt, in
         __syncthreads();
     }
     if (I < 0) return;
-    // the pairs leave through a tile of LDS of the wave's own, in a rolled loop (unrolled, the stores
-    // were two thirds of the kernel's code)
     const int64_t nbb = (int64_t)nb * nb;
-    const bool part = pl.nsplit > 1;
-    float *out = part ? partial + ((int64_t)(blk - whole) * pl.nsplit + pl.split) * nbb : t.A[mat] + (blk - t.first[mat]) * nbb;
-    PairTile &tile = *(PairTile *)(lds + wave * sizeof(PairTile));
-#pragma unroll 1
-    for (int p = 0; p < 8; ++p) {
-        const int i0 = 32 * (2 * I + (p >> 2)), j0 = 32 * (4 * J + (p & 3));
-        if (i0 >= nb || j0 > i0) continue;
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-            if (q == p)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) tile[acc_row(r, lane)][col] = acc[q >> 2][q & 3][r];
-        __builtin_amdgcn_wave_barrier();
-        store_pair(out, nb, i0, j0, tile, part, beta, scale);
-        __builtin_amdgcn_wave_barrier();
+    float av[2][16];
+    if (pl.nsplit > 1) {
+        float *out = partial + ((int64_t)(blk - whole) * pl.nsplit + pl.split) * nbb;
+#define DOBB_MX4_STORE(p)                                                                                            \
+        {                                                                                                            \
+            const int i0 = 32 * (2 * I + ((p) >> 2)), j0 = 32 * (4 * J + ((p) & 3));                                  \
+            if (i0 < nb && j0 <= i0) store_pair(out, nb, i0, j0, acc[(p) >> 2][(p) & 3], av[0], true, beta, scale);    \
+        }
+        DOBB_MX4_STORE(0) DOBB_MX4_STORE(1) DOBB_MX4_STORE(2) DOBB_MX4_STORE(3)
+        DOBB_MX4_STORE(4) DOBB_MX4_STORE(5) DOBB_MX4_STORE(6) DOBB_MX4_STORE(7)
+#undef DOBB_MX4_STORE
+        return;
     }
+    // pair by pair, the old entries of the next one read before the stores of this one
+    float *out = t.A[mat] + (blk - t.first[mat]) * nbb;
+    const bool old = beta > 0.0;
+    if (old) read_pair(out, nb, 64 * I, 128 * J, av[0]);
+#define DOBB_MX4_STORE(p)                                                                                            \
+    {                                                                                                                \
+        const int i0 = 32 * (2 * I + ((p) >> 2)), j0 = 32 * (4 * J + ((p) & 3));                                      \
+        if (old && (p) < 7) read_pair(out, nb, 32 * (2 * I + (((p) + 1) >> 2)), 32 * (4 * J + (((p) + 1) & 3)), av[((p) + 1) & 1]); \
+        batch();                                                                                                     \
+        if (i0 < nb && j0 <= i0) store_pair(out, nb, i0, j0, acc[(p) >> 2][(p) & 3], av[(p) & 1], false, beta, scale); \
+        batch();                                                                                                     \
+    }
+    DOBB_MX4_STORE(0) DOBB_MX4_STORE(1) DOBB_MX4_STORE(2) DOBB_MX4_STORE(3)
+    DOBB_MX4_STORE(4) DOBB_MX4_STORE(5) DOBB_MX4_STORE(6) DOBB_MX4_STORE(7)
+#undef DOBB_MX4_STORE
 }
 
 // The splits' sums of one 32 x 32 pair in fp64, in split order, for blocks whole .. of a launch; one
 // workgroup a pair, thread t with column t % 32 and rows t / 32 + 8 u
 __global__ void __launch_bounds__(256) k_moment_mx4_reduce(int cnt, int nb, int whole, int nsplit, int pairs, double beta,
                                                            double scale, const float *partial, MomentTable t) {
-    __shared__ PairTile tile;
+    __shared__ float tile[32][kPairPad];
     const int64_t nbb = (int64_t)nb * nb;
     const int blk = whole + blockIdx.x / pairs;
     int fi = 0, fj = blockIdx.x % pairs;
