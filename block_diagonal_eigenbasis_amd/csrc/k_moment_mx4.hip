@@ -497,20 +497,22 @@ hipError_t launch_wide(const MomentMx4Args &a, const MomentTable &t, unsigned gr
 
 // How a launch over `blocks` blocks splits their tokens: the plan that an estimate of the time makes
 // smallest.  A launch runs in rounds of workgroups over the chip's slots (two narrow workgroups or one
-// wide one a CU); a tile pair takes a workgroup about 0.6 us (narrow; 1.4 us and more where all slots
-// read at once) or 2.2 us (wide).  Whole rounds of blocks are left whole; those of the last round, which
-// would leave slots empty, may be split, for the partial sums' traffic and a launch of 6 us.  Never more
-// tile pairs than kSplitPairs in one go, never a split with none.
+// wide one a CU).  A tile pair takes a narrow workgroup 0.26 us (four at once; 1.8 us at 128 columns where all
+// slots read at the memory's rate), a wide one 0.6 us and 0.1 us a fragment.  Whole rounds of blocks are
+// left whole; those of the last round, which would leave slots empty, may be split, for the partial sums'
+// traffic and a second launch (5 us).  Never more tile pairs than kSplitPairs in one go, never a split with
+// none.  Measured, whole against split: 16384 tokens, 576 blocks of 100: 110 and 104 us; 192 blocks of 400: 320
+// and 285; 48 blocks of 400: 116 and 84; 4096 tokens, 4 blocks of 192: 24 and 15; 192 blocks of 128: 18 and 25.
 MomentPlan moment_mx4_plan(int64_t nb, int64_t blocks, int64_t tiles) {
     const int64_t tp = (tiles + 1) / 2;
     const bool narrow = nb <= kNarrow;
     const int64_t nwg = narrow ? 1 : wide_wgs(nb), slots = narrow ? 512 : 256;
-    const double partial = (double)nb * nb * 8 / 5e6;
+    const double partial = (double)nb * nb * 8 / 5e6, tau = narrow ? 0.26 : 0.6 + 0.1 * (double)((nb + 31) / 32);
     auto run = [&](int64_t wgs, int64_t pairs) {           // us of wgs workgroups of so many tile pairs
         double t = 0.0;
         for (; wgs > 0; wgs -= std::min(wgs, slots)) {
             const double full = (double)std::min(wgs, slots) / 512 * 1.8 * nb / 128;
-            t += narrow ? std::max({0.6 * ((pairs + 3) / 4) * 4, full * pairs, 2.4}) : 2.2 * pairs;
+            t += narrow ? std::max(tau * ((pairs + 3) / 4) * 4, full * pairs) : tau * pairs;
             if (wgs > 64 * slots) return t * (double)wgs / slots;
         }
         return t;
@@ -526,7 +528,7 @@ MomentPlan moment_mx4_plan(int64_t nb, int64_t blocks, int64_t tiles) {
             const int64_t per = (tp + ns - 1) / ns;
             if ((tp + per - 1) / per != ns) continue;
             const double c = run(whole * nwg, tp) + (rest ? run(rest * nwg * ns, per) : 0.0) +
-                             (rest && ns > 1 ? 6.0 + partial * (double)(rest * ns) : 0.0);
+                             (rest && ns > 1 ? 5.0 + partial * (double)(rest * ns) : 0.0);
             if (c < cost) { best = rest && ns > 1 ? MomentPlan{(int)whole, (int)ns} : MomentPlan{(int)blocks, 1}; cost = c; }
         }
     }
