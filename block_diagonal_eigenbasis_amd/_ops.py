@@ -58,15 +58,20 @@ def _lib() -> ctypes.CDLL:
     return L
 
 
-def _call(fn, stream, *args):
-    """fn(*args) with `stream` current; what it returns beside the status is then kept from reuse until the
-    stream that was current before is done with it."""
+def _call(fn, stream, of, *args):
+    """fn(of, *args) with `stream` current; what it returns beside the status is then kept from reuse until
+    the stream that was current before is done with it.  `of` is a tensor or a list of them."""
     if stream is None:
-        return fn(*args)
+        return fn(of, *args)
+    if not isinstance(of, torch.Tensor):
+        of = list(of)
+    first = of if isinstance(of, torch.Tensor) else of[0] if of else None
+    if isinstance(first, torch.Tensor) and first.device != stream.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
     with torch.cuda.device(stream.device):
         before = torch.cuda.current_stream()
         with torch.cuda.stream(stream):
-            got = fn(*args)
+            got = fn(of, *args)
     if isinstance(got, tuple):
         for t in got[1:]:
             t.record_stream(before)
@@ -79,7 +84,7 @@ def dobb_grad_norm_grouped(Gs, norms: torch.Tensor | None = None, total: torch.T
     """The l2 norm of all entries of the list Gs (contiguous, fp32 or bf16, mixed; a tensor listed twice
     counts twice) into `total` (fp32 scalar, returned) and, if given, each tensor's into `norms` (fp32,
     one entry a tensor).  Sums are formed in fp64.  Nothing is synchronized."""
-    st, total = _call(_host().grads, stream, 0, Gs, None, 0.0, norms, total, ws)
+    st, total = _call(_host().grads, stream, Gs, 0, None, 0.0, norms, total, ws)
     _check(st, "dobb_grad_norm_grouped")
     return total
 
@@ -87,7 +92,7 @@ def dobb_grad_norm_grouped(Gs, norms: torch.Tensor | None = None, total: torch.T
 def dobb_clip_grads_grouped(Gs, total: torch.Tensor, max_norm: float, outs=None, stream=None) -> None:
     """outs[i] <- Gs[i] * min(1, max_norm / (total + 1e-6)), in place without outs; total is a device
     scalar (fp32).  Buffers written may not overlap: a tensor listed twice in place is refused."""
-    st, _ = _call(_host().grads, stream, 1, Gs, outs, max_norm, None, total, None)
+    st, _ = _call(_host().grads, stream, Gs, 1, outs, max_norm, None, total, None)
     _check(st, "dobb_clip_grads_grouped")
 
 
@@ -96,7 +101,7 @@ def dobb_clip_grad_norm_grouped(Gs, max_norm: float, outs=None, norms: torch.Ten
                                 stream=None) -> torch.Tensor:
     """dobb_grad_norm_grouped, then dobb_clip_grads_grouped with its total, in one call; returns total
     (the norm before clipping)."""
-    st, total = _call(_host().grads, stream, 2, Gs, outs, max_norm, norms, total, ws)
+    st, total = _call(_host().grads, stream, Gs, 2, outs, max_norm, norms, total, ws)
     _check(st, "dobb_clip_grad_norm_grouped")
     return total
 

@@ -14,6 +14,16 @@ constexpr int64_t kMaxNb = 1024;
 constexpr int64_t kMaxN = (int64_t)1 << 24;       // the product's column offsets are 32-bit
 constexpr int64_t kMaxTokens = (int64_t)1 << 40;
 
+// nothing thrown inside (host memory for the lists) leaves a C entry
+template <typename F>
+dobb_status guarded(F f) {
+    try {
+        return f();
+    } catch (...) {
+        return DOBB_ERR_INVALID_ARG;
+    }
+}
+
 bool dtype_ok(dobb_dtype d) { return d == DOBB_F32 || d == DOBB_BF16; }
 int64_t size_of(dobb_dtype d) { return d == DOBB_BF16 ? 2 : 4; }
 inline size_t al256(size_t x) { return (x + 255) / 256 * 256; }
@@ -73,15 +83,26 @@ bool apart(std::vector<Span> &v) {
 
 // Every buffer written is the tensor it is made from (same type) or apart from everything else in the
 // list: a chunk of one is then read and written by one workgroup only.
-dobb_status check_outputs(const GradArgs &a) {
+// norms, total: written too where `sums` (read, total, where not); ws_bytes of ws likewise.
+dobb_status check_outputs(const GradArgs &a, const float *norms, const float *total, bool sums, const void *ws, size_t ws_bytes) {
     std::vector<Span> v;
-    v.reserve(2 * (size_t)a.count);
+    v.reserve(2 * (size_t)a.count + 3);
+    auto add = [&](const void *p, size_t bytes, bool out) {
+        if (p && bytes) v.push_back({(uintptr_t)p, (uintptr_t)p + bytes, out});
+    };
     for (int i = 0; i < a.count; ++i) {
         if (a.numel[i] == 0) continue;
+        if (!a.out) {
+            add(a.G[i], (size_t)(a.numel[i] * size_of(a.g_dtypes[i])), false);
+            continue;
+        }
         const uintptr_t g = (uintptr_t)a.G[i], o = (uintptr_t)a.out[i];
         if (g != o || a.g_dtypes[i] != a.out_dtypes[i]) v.push_back({g, g + (uintptr_t)(a.numel[i] * size_of(a.g_dtypes[i])), false});
         v.push_back({o, o + (uintptr_t)(a.numel[i] * size_of(a.out_dtypes[i])), true});
     }
+    add(norms, 4 * (size_t)a.count, sums);
+    add(total, 4, sums);
+    add(ws, ws_bytes, true);
     return apart(v) ? DOBB_OK : DOBB_ERR_INVALID_ARG;
 }
 
@@ -90,8 +111,7 @@ dobb_status check_clip(const GradArgs &a, const float *total, float max_norm) {
     if (st != DOBB_OK) return st;
     st = check_list(a.count, a.numel, (const void *const *)a.out, a.out_dtypes);
     if (st != DOBB_OK) return st;
-    if (!total || !(max_norm >= 0.f)) return DOBB_ERR_INVALID_ARG;
-    return check_outputs(a);
+    return total && max_norm >= 0.f ? DOBB_OK : DOBB_ERR_INVALID_ARG;
 }
 
 size_t norm_ws(int count, const int64_t *numel, const dobb_dtype *dt) {
@@ -157,6 +177,16 @@ dobb_status moment_grouped(int count, const dobb_shape *shapes, const void *cons
         if (!codes[i] || !scales[i] || !A[i] || ((uintptr_t)codes[i] & 15u) || ((uintptr_t)scales[i] & 3u) || ((uintptr_t)A[i] & 3u))
             return DOBB_ERR_INVALID_ARG;
     }
+    // moments are written: no two the same, and none over a capture (captures may be shared)
+    std::vector<Span> spans;
+    spans.reserve(3 * (size_t)count);
+    for (int i = 0; i < count; ++i) {
+        auto add = [&](const void *p, int64_t bytes, bool out) { spans.push_back({(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes, out}); };
+        add(A[i], 4 * shapes[i].n * shapes[i].nb, true);
+        add(codes[i], 64 * tiles * shapes[i].n, false);
+        add(scales[i], 4 * tiles * shapes[i].n, false);
+    }
+    if (!apart(spans)) return DOBB_ERR_INVALID_ARG;
     const std::vector<MomentLaunch> launches = moment_launches(count, shapes);
     const dobb_status st = check_ws(ws, ws_bytes, moment_ws(launches, tiles));
     if (st != DOBB_OK) return st;
@@ -186,16 +216,6 @@ dobb_status moment_grouped(int count, const dobb_shape *shapes, const void *cons
     return DOBB_OK;
 }
 
-// nothing thrown inside (host memory for the lists) leaves a C entry
-template <typename F>
-dobb_status guarded(F f) {
-    try {
-        return f();
-    } catch (...) {
-        return DOBB_ERR_INVALID_ARG;
-    }
-}
-
 }  // namespace
 
 extern "C" {
@@ -209,13 +229,18 @@ size_t dobb_grad_norm_workspace_size(int count, const int64_t *numel, const dobb
 
 dobb_status dobb_grad_norm_grouped(int count, const int64_t *numel, const void *const *G, const dobb_dtype *g_dtypes,
                                    float *norms, float *total, void *ws, size_t ws_bytes, dobb_stream_t stream) {
-    dobb_status st = check_list(count, numel, G, g_dtypes);
-    if (st != DOBB_OK) return st;
-    if (!total) return DOBB_ERR_INVALID_ARG;
-    st = check_ws(ws, ws_bytes, norm_ws(count, numel, g_dtypes));
-    if (st != DOBB_OK) return st;
-    const GradArgs a{count, numel, G, g_dtypes, nullptr, nullptr};
-    return hip_status(launch_grad_norm(a, norms, total, (double *)ws, (hipStream_t)stream));
+    return guarded([&]() -> dobb_status {
+        dobb_status st = check_list(count, numel, G, g_dtypes);
+        if (st != DOBB_OK) return st;
+        if (!total) return DOBB_ERR_INVALID_ARG;
+        const GradArgs a{count, numel, G, g_dtypes, nullptr, nullptr};
+        const size_t need = norm_ws(count, numel, g_dtypes);
+        st = check_outputs(a, norms, total, true, ws, need);
+        if (st != DOBB_OK) return st;
+        st = check_ws(ws, ws_bytes, need);
+        if (st != DOBB_OK) return st;
+        return hip_status(launch_grad_norm(a, norms, total, (double *)ws, (hipStream_t)stream));
+    });
 }
 
 dobb_status dobb_clip_grads_grouped(int count, const int64_t *numel, const void *const *G, const dobb_dtype *g_dtypes,
@@ -223,7 +248,8 @@ dobb_status dobb_clip_grads_grouped(int count, const int64_t *numel, const void 
                                     dobb_stream_t stream) {
     return guarded([&]() -> dobb_status {
         const GradArgs a{count, numel, G, g_dtypes, out, out_dtypes};
-        const dobb_status st = check_clip(a, total, max_norm);
+        dobb_status st = check_clip(a, total, max_norm);
+        if (st == DOBB_OK) st = check_outputs(a, nullptr, total, false, nullptr, 0);
         if (st != DOBB_OK) return st;
         return hip_status(launch_grad_clip(a, total, max_norm, (hipStream_t)stream));
     });
@@ -236,7 +262,10 @@ dobb_status dobb_clip_grad_norm_grouped(int count, const int64_t *numel, const v
         const GradArgs a{count, numel, G, g_dtypes, out, out_dtypes};
         dobb_status st = check_clip(a, total, max_norm);
         if (st != DOBB_OK) return st;
-        st = check_ws(ws, ws_bytes, norm_ws(count, numel, g_dtypes));
+        const size_t need = norm_ws(count, numel, g_dtypes);
+        st = check_outputs(a, norms, total, true, ws, need);
+        if (st != DOBB_OK) return st;
+        st = check_ws(ws, ws_bytes, need);
         if (st != DOBB_OK) return st;
         st = hip_status(launch_grad_norm(a, norms, total, (double *)ws, (hipStream_t)stream));
         if (st != DOBB_OK) return st;

@@ -27,7 +27,9 @@ struct TypeErr : std::runtime_error { using std::runtime_error::runtime_error; }
 
 const Tensor &gpu(PyObject *o, const char *name) {
     if (!THPVariable_Check(o) || !THPVariable_Unpack(o).is_cuda()) throw TypeErr(std::string(name) + " must be a GPU tensor");
-    return THPVariable_Unpack(o);
+    const Tensor &t = THPVariable_Unpack(o);
+    if (t.is_neg()) throw std::invalid_argument(std::string(name) + " is a negated view: resolve it first");
+    return t;
 }
 
 const Tensor &gpu_on(PyObject *o, const char *name, c10::Device dev) {
@@ -130,12 +132,12 @@ PyObject *guarded(F f) {
 
 PyObject *own(const Tensor &t) { return THPVariable_Wrap(t); }
 
-// grads(mode, Gs, outs, max_norm, norms, total, ws) -> (status, total); mode 0: norm, 1: clip by total, 2: both
+// grads(Gs, mode, outs, max_norm, norms, total, ws) -> (status, total); mode 0: norm, 1: clip by total, 2: both
 PyObject *py_grads(PyObject *, PyObject *args) {
     int mode;
     double max_norm;
     PyObject *gs, *os, *norms, *total, *ws;
-    if (!PyArg_ParseTuple(args, "iOOdOOO", &mode, &gs, &os, &max_norm, &norms, &total, &ws)) return nullptr;
+    if (!PyArg_ParseTuple(args, "OiOdOOO", &gs, &mode, &os, &max_norm, &norms, &total, &ws)) return nullptr;
     return guarded([&]() -> PyObject * {
         List g(gs, "Gs", nullptr);
         const c10::Device dev = g.at(0).device();

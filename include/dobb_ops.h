@@ -34,8 +34,9 @@ extern "C" {
  * norms: device fp32 [count] or NULL.  total: device fp32 scalar.
  * Clipping multiplies in fp32 and rounds to out's type once, to nearest even.  out[i] is G[i] itself
  * with the same dtype (in place: a coefficient of 1 then writes nothing) or a buffer of its own in
- * out_dtypes[i] (fp32 or bf16).  Buffers written must not overlap each other or any other tensor of
- * the list; a list that breaks this (one tensor listed twice in place, say) is DOBB_ERR_INVALID_ARG.
+ * out_dtypes[i] (fp32 or bf16).  Buffers written (norms, total and the workspace among them) must
+ * not overlap each other or any other tensor of the list; a call that breaks this (one tensor listed twice
+ * in place, say) is DOBB_ERR_INVALID_ARG.
  * max_norm >= 0, infinity allowed.  dobb_clip_grads_grouped takes the total from device memory, so a
  * caller may combine totals over processes in between; dobb_clip_grad_norm_grouped is the two in a row.
  * -------------------------------------------------------------------------------------------------*/
@@ -80,7 +81,8 @@ size_t dobb_moment_mx4_workspace_size(int count, const dobb_shape *shapes, int64
 dobb_status dobb_accumulate_moment_mx4(const dobb_shape *s, const void *codes, const void *scales, int64_t tiles,
                                        int64_t N, float beta, float *A, void *ws, size_t ws_bytes,
                                        dobb_stream_t stream);
-/* The same for a matrix set; shapes and pointer arrays are host arrays of length count. */
+/* The same for a matrix set; shapes and pointer arrays are host arrays of length count.  Captures may be
+ * shared by several matrices; moments that overlap each other or a capture are DOBB_ERR_INVALID_ARG. */
 dobb_status dobb_accumulate_moment_mx4_grouped(int count, const dobb_shape *shapes, const void *const *codes,
                                                const void *const *scales, int64_t tiles, int64_t N, float beta,
                                                float *const *A, void *ws, size_t ws_bytes, dobb_stream_t stream);

@@ -269,3 +269,25 @@ def test_refusals():
         dobb.dobb_clip_grad_norm_grouped([t], -1.0)
     with pytest.raises(dobb.DobbError):
         dobb.dobb_clip_grad_norm_grouped([t], math.nan)
+
+
+def test_sums_over_a_gradient_are_refused():
+    t = torch.zeros(64, device=DEV)
+    with pytest.raises(dobb.DobbError):
+        dobb.dobb_grad_norm_grouped([t], total=t[3])
+    with pytest.raises(dobb.DobbError):
+        dobb.dobb_clip_grad_norm_grouped([t], 1.0, norms=t[:1])
+    with pytest.raises(dobb.DobbError):
+        dobb.dobb_clip_grads_grouped([t], t[63:], 1.0)
+
+
+def test_iterables_and_integer_bounds():
+    ts, _ = views([50, 60], [F32, BF16], 30)
+    want = dobb.dobb_grad_norm_grouped(ts)
+    assert torch.equal(dobb.dobb_grad_norm_grouped(t for t in ts), want)
+    assert torch.equal(dobb.dobb_clip_grad_norm_grouped(tuple(ts), 10 ** 6), want)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    total = dobb.dobb_grad_norm_grouped((t for t in ts), stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(total, want)

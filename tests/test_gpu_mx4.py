@@ -354,3 +354,40 @@ def test_refusals():
         dobb.dobb_accumulate_moment_mx4(codes, scales, A, 64, 200, 1.0)
     with pytest.raises(ValueError, match="number of tiles"):
         dobb.dobb_accumulate_moment_mx4_grouped([codes, codes[:1]], [scales, scales[:1]], [A, A.clone()], [64, 64], 100)
+
+
+def test_shared_captures_and_repeated_moments():
+    """One capture for several weights (q, k and v see the same activations) is in order; one moment listed
+    twice would be written by two workgroups and is refused."""
+    codes, scales = dobb.dobb_mx4_quantize(activations(300, 128, 2, BF16))
+    As = [torch.empty(2, 64, 64, device=DEV) for _ in range(3)]
+    dobb.dobb_accumulate_moment_mx4_grouped([codes] * 3, [scales] * 3, As, [64] * 3, 300)
+    assert torch.equal(As[0], As[1]) and torch.equal(As[0], As[2])
+    check_moment(As[0], host(dobb.dobb_mx4_dequantize(codes, scales, 300)), 64, 300, 0.0, 0.0, 3)
+    with pytest.raises(dobb.DobbError):
+        dobb.dobb_accumulate_moment_mx4_grouped([codes] * 2, [scales] * 2, [As[0], As[0]], [64] * 2, 300)
+
+
+def test_two_captures_at_once_on_two_streams():
+    xs = [activations(3000, 400, 80 + i, BF16) for i in range(2)]
+    want = []
+    for x in xs:
+        c, s = dobb.dobb_mx4_quantize(x)
+        want.append(dobb.dobb_accumulate_moment_mx4(c, s, torch.empty(1, 400, 400, device=DEV), 400, 3000))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [torch.empty(1, 400, 400, device=DEV) for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for x, st, A in zip(xs, streams, got):
+            c, s = dobb.dobb_mx4_quantize(x, stream=st)
+            dobb.dobb_accumulate_moment_mx4(c, s, A, 400, 3000, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_negated_views_are_refused():
+    x = torch.randn(40, 8, dtype=torch.complex64, device=DEV).conj().imag
+    assert x.is_neg()
+    with pytest.raises(ValueError, match="negated view"):
+        dobb.dobb_mx4_quantize(x)

@@ -40,7 +40,7 @@ def _ptr(*v):
     return (ctypes.c_void_p * len(v))(*v)
 
 
-def _norm(numel=(64, 10), G=(FAKE, FAKE + 0x1000), dt=(0, 1), total=FAKE, ws=FAKE, wsb=1 << 20, count=None):
+def _norm(numel=(64, 10), G=(FAKE, FAKE + 0x1000), dt=(0, 1), total=0x80000, ws=0x90000, wsb=1 << 20, count=None):
     return _ops._lib().dobb_grad_norm_grouped(len(numel) if count is None else count, _i64(*numel), _ptr(*G), _int(*dt),
                                               None, total, ws, wsb, None)
 
@@ -54,7 +54,7 @@ def test_grad_norm_refusals():
     assert _norm(dt=(0, 2)) == DTYPE
     assert _norm(numel=(64, -1)) == SHAPE
     assert _norm(ws=None) == WORKSPACE
-    assert _norm(ws=FAKE + 16) == WORKSPACE
+    assert _norm(ws=0x90010) == WORKSPACE
     assert _norm(wsb=8) == WORKSPACE
     size = _ops._lib().dobb_grad_norm_workspace_size
     assert size(2, _i64(64, 10), _int(0, 1)) >= 8 * 2
@@ -91,11 +91,27 @@ def test_clip_refusals():
     assert _clip(odt=(1, 0)) == INVALID
     # one long buffer around several shorter ones
     assert _clip(numel=(4096, 16), G=(0x20000, 0x10000), out=(0x40000, 0x40000 + 8192)) == INVALID
+    # the total among what is written, or read, and the sums and the workspace over a gradient
+    assert _clip(total=FAKE + 8) == INVALID
+    lib, one = _ops._lib(), (1, _i64(64), _ptr(FAKE), _int(0))
+    assert lib.dobb_grad_norm_grouped(*one, None, FAKE + 252, 0x40000, 1 << 20, None) == INVALID
+    assert lib.dobb_grad_norm_grouped(*one, FAKE, 0x80000, 0x40000, 1 << 20, None) == INVALID
+    assert lib.dobb_grad_norm_grouped(*one, 0x80000, 0x80000, 0x40000, 1 << 20, None) == INVALID
+    assert lib.dobb_grad_norm_grouped(*one, None, 0x80000, FAKE, 1 << 20, None) == INVALID
+    assert lib.dobb_clip_grad_norm_grouped(*one, _ptr(0x20000), _int(0), 1.0, None, 0x80000, 0x20000, 1 << 20, None) == INVALID
+    # many separate allocations, in no order: the same answers
+    import random
+    at = [0x100000 + 0x1000 * i for i in range(400)]
+    random.Random(1).shuffle(at)
+    many = dict(numel=(64,) * 400, G=tuple(at), dt=(0,) * 400, odt=(0,) * 400)
+    assert _clip(**many, out=tuple(a if i != 399 else at[17] for i, a in enumerate(at))) == INVALID
+    a = (400, _i64(*many["numel"]), _ptr(*at), _int(*many["dt"]), _ptr(*at), _int(*many["odt"]))
+    assert lib.dobb_clip_grad_norm_grouped(*a, 1.0, None, 0x40000, None, 0, None) == WORKSPACE      # this list is in order
     # the bad list of a call is refused with its workspace in order too
     bad = (2, _i64(64, 64), _ptr(FAKE, FAKE), _int(0, 0), _ptr(FAKE, FAKE), _int(0, 0))
     assert _ops._lib().dobb_clip_grad_norm_grouped(*bad, 1.0, None, FAKE, FAKE, 1 << 20, None) == INVALID
     good = (2, _i64(64, 64), _ptr(FAKE, FAKE + 256), _int(0, 0), _ptr(FAKE, FAKE + 256), _int(0, 0))
-    assert _ops._lib().dobb_clip_grad_norm_grouped(*good, 1.0, None, FAKE, None, 0, None) == WORKSPACE
+    assert _ops._lib().dobb_clip_grad_norm_grouped(*good, 1.0, None, 0x80000, None, 0, None) == WORKSPACE
 
 
 def test_mx4_refusals():
@@ -128,7 +144,16 @@ def test_moment_mx4_refusals():
         assert call(s=_abi.Shape(1, n, nb)) == SHAPE
     need = dobb.dobb_moment_mx4_workspace_size([(1, 768, 192)], 64)
     assert need > 0 and need % 256 == 0
-    assert call() == WORKSPACE and call(ws=FAKE, wsb=need - 1) == WORKSPACE and call(ws=FAKE + 64, wsb=need) == WORKSPACE
+    two = (_abi.Shape * 2)(_abi.Shape(1, 768, 192), _abi.Shape(1, 768, 192))
+    grouped = L.dobb_accumulate_moment_mx4_grouped
+    size_a, size_c = 768 * 192 * 4, 64 * 64 * 768
+    C, S, A = 0x10000000, 0x20000000, 0x30000000
+    assert grouped(2, two, _ptr(C, C), _ptr(S, S), 64, 8192, 0.5, _ptr(A, A), None, 0, None) == INVALID          # one moment twice
+    assert grouped(2, two, _ptr(C, C), _ptr(S, S), 64, 8192, 0.5, _ptr(A, A + size_a - 4), None, 0, None) == INVALID
+    assert grouped(2, two, _ptr(C, C), _ptr(S, S), 64, 8192, 0.5, _ptr(A, C + size_c - 4), None, 0, None) == INVALID
+    assert grouped(2, two, _ptr(C, C), _ptr(S, S), 64, 8192, 0.5, _ptr(A, A + size_a), None, 0, None) == WORKSPACE  # a shared capture
+    assert call(codes=C, scales=S, A=A) == WORKSPACE
+    assert call(codes=C, scales=S, A=A, ws=FAKE, wsb=need - 1) == WORKSPACE and call(codes=C, scales=S, A=A, ws=FAKE + 64, wsb=need) == WORKSPACE
     size = dobb.dobb_moment_mx4_workspace_size
     assert size([(1, 768, 100)], 8) == 0 and size([(1, 768, 192)], 0) == 0
     # one tile has nothing to split; a long capture is split whatever the grid
