@@ -18,6 +18,10 @@ constexpr int kFinishMats = 900;
 constexpr int kUnroll = 4;       // 16-byte vectors in flight per thread
 constexpr int kThreads = 256;
 constexpr int64_t kStep = (int64_t)kThreads * kUnroll;   // vectors a workgroup reads at a time
+// Clipping: one workgroup for every step of 8 KB.  Workgroups of four steps of 16 KB took 1.62 ms for the call
+// on the GPT-2 XL set in bf16, of one such step 1.51, of one of 8 KB 1.50 (4 KB: 1.53).
+constexpr int kClipUnroll = 2;
+constexpr int64_t kClipStep = (int64_t)kThreads * kClipUnroll;
 
 struct NormTable {
     const void *g[kNormMats];
@@ -177,24 +181,24 @@ __device__ __forceinline__ void scale_chunk(const char *g, char *o, int64_t nume
         *(Out *)(o + p * OB) = r;
     };
     int64_t b = v0;
-    for (; b + kStep <= end; b += kStep) {              // whole steps: no bounds to check
-        Vec16 x[kUnroll];
+    for (; b + kClipStep <= end; b += kClipStep) {              // whole steps: no bounds to check
+        Vec16 x[kClipUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) x[u] = *(const Vec16 *)(g + (b + u * kThreads + threadIdx.x) * 16);
+        for (int u = 0; u < kClipUnroll; ++u) x[u] = *(const Vec16 *)(g + (b + u * kThreads + threadIdx.x) * 16);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) put(b + u * kThreads + threadIdx.x, x[u]);
+        for (int u = 0; u < kClipUnroll; ++u) put(b + u * kThreads + threadIdx.x, x[u]);
     }
     if (b < end) {
-        Vec16 x[kUnroll];
+        Vec16 x[kClipUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {             // places past the end read the last vector, for nothing
+        for (int u = 0; u < kClipUnroll; ++u) {             // places past the end read the last vector, for nothing
             const int64_t p = b + u * kThreads + threadIdx.x;
             x[u] = *(const Vec16 *)(g + (p < end ? p : end - 1) * 16);
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
+        for (int u = 0; u < kClipUnroll; ++u) {
             const int64_t p = b + u * kThreads + threadIdx.x;
             if (p < end) put(p, x[u]);
         }
@@ -294,11 +298,7 @@ hipError_t launch_grad_norm(const GradArgs &a, float *norms, float *total, doubl
 }
 
 hipError_t launch_grad_clip(const GradArgs &a, const float *total, float max_norm, hipStream_t s) {
-    // vectors per workgroup: one step where that gives no more workgroups than run at once, up to four
-    int64_t all = 0;
-    for (int i = 0; i < a.count; ++i) all += vectors(a.numel[i], a.g_dtypes[i]);
-    const int64_t steps = all / (kStep * 2048);
-    const int64_t nv = (steps < 1 ? 1 : steps > 4 ? 4 : steps) * kStep;
+    const int64_t nv = kClipStep;
     for (int i0 = 0; i0 < a.count;) {
         ClipTable t{};
         int64_t chunks = 0;
