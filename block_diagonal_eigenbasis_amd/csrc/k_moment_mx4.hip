@@ -497,7 +497,7 @@ hipError_t launch_wide(const MomentMx4Args &a, const MomentTable &t, unsigned gr
 
 // How a launch over `blocks` blocks splits their tokens: the plan that an estimate of the time makes
 // smallest.  A launch runs in rounds of workgroups over the chip's slots (two narrow workgroups or one
-// wide one a CU).  A tile pair takes a narrow workgroup 0.26 us (four at once; 1.8 us at 128 columns where all
+// wide one a CU).  A tile pair takes a narrow workgroup 0.34 us (four at once; 1.8 us at 128 columns where all
 // slots read at the memory's rate), a wide one 0.6 us and 0.1 us a fragment.  Whole rounds of blocks are
 // left whole; those of the last round, which would leave slots empty, may be split, for the partial sums'
 // traffic and a second launch (5 us).  Never more tile pairs than kSplitPairs in one go, never a split with
@@ -507,7 +507,7 @@ MomentPlan moment_mx4_plan(int64_t nb, int64_t blocks, int64_t tiles) {
     const int64_t tp = (tiles + 1) / 2;
     const bool narrow = nb <= kNarrow;
     const int64_t nwg = narrow ? 1 : wide_wgs(nb), slots = narrow ? 512 : 256;
-    const double partial = (double)nb * nb * 8 / 5e6, tau = narrow ? 0.26 : 0.6 + 0.1 * (double)((nb + 31) / 32);
+    const double partial = (double)nb * nb * 8 / 5e6, tau = narrow ? 0.34 : 0.6 + 0.1 * (double)((nb + 31) / 32);
     auto run = [&](int64_t wgs, int64_t pairs) {           // us of wgs workgroups of so many tile pairs
         double t = 0.0;
         for (; wgs > 0; wgs -= std::min(wgs, slots)) {
