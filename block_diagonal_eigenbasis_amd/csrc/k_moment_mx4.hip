@@ -10,11 +10,14 @@
 //
 // k_moment_mx4_narrow (nb <= 128): a block's codes are read from HBM once, straight into operand
 //   registers.  A workgroup owns one block; its four waves take every fourth tile pair, keep all
-//   fragment pairs on or below the diagonal in registers and add up through LDS at the end.
+//   fragment pairs on or below the diagonal in registers and hand each other their sums through LDS at the
+//   end.  Bound by HBM: 576 blocks of 100, 16384 tokens (501 MB of codes), in 108 us, 5.3 TB/s with A.
 // k_moment_mx4_wide (128 < nb <= 1024): a workgroup of 8 waves stages the tile pair of a whole block
 //   in LDS (through registers, one stage ahead) and each wave owns 2 x 4 of the fragment pairs on or
 //   below the diagonal; a block with more than 8 such groups takes several workgroups, neighbours on one
-//   XCD, so that its codes come from HBM once and from that XCD's L2 after that.
+//   XCD, so that its codes come from HBM once and from that XCD's L2 after that.  192 blocks of 400, 16384
+//   tokens, in 252 us; bound by the matrix cores' power: the clock falls to 1.8 GHz, and codes that are all
+//   zero take a third less time.
 // Rounding: fp32 sums of at most 4096 (narrow, then four of those in fp32) or 16384 tokens (wide) in
 // the accumulators, token splits in fp64 (k_moment_mx4_reduce).
 #include <algorithm>
