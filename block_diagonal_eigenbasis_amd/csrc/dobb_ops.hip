@@ -126,7 +126,12 @@ dobb_status check_capture(int64_t N, int64_t n, const void *p, dobb_dtype dt, in
     if ((N / kMx4Tile + 1) * ((n + 127) / 128) > 0x7fffffff) return DOBB_ERR_SHAPE;
     if (((uintptr_t)codes & 15u) || ((uintptr_t)scales & 3u) || ((uintptr_t)p & (uintptr_t)(size_of(dt) - 1)))
         return DOBB_ERR_INVALID_ARG;
-    return DOBB_OK;
+    // values, codes and scales are three buffers, whichever of them is written
+    auto span = [](const void *q, uintptr_t bytes) { return Span{(uintptr_t)q, (uintptr_t)q + bytes, true}; };
+    const uintptr_t cells = (uintptr_t)((N + kMx4Tile - 1) / kMx4Tile) * (uintptr_t)n;
+    std::vector<Span> v{span(p, ((uintptr_t)(N - 1) * (uintptr_t)ld + (uintptr_t)n) * (uintptr_t)size_of(dt)), span(codes, 64 * cells),
+                        span(scales, 4 * cells)};
+    return apart(v) ? DOBB_OK : DOBB_ERR_INVALID_ARG;
 }
 
 dobb_status check_moment_shape(const dobb_shape &s) {
@@ -177,18 +182,20 @@ dobb_status moment_grouped(int count, const dobb_shape *shapes, const void *cons
         if (!codes[i] || !scales[i] || !A[i] || ((uintptr_t)codes[i] & 15u) || ((uintptr_t)scales[i] & 3u) || ((uintptr_t)A[i] & 3u))
             return DOBB_ERR_INVALID_ARG;
     }
-    // moments are written: no two the same, and none over a capture (captures may be shared)
+    const std::vector<MomentLaunch> launches = moment_launches(count, shapes);
+    const size_t need = moment_ws(launches, tiles);
+    // moments and the workspace are written: no two the same, and none over a capture (captures may be shared)
     std::vector<Span> spans;
-    spans.reserve(3 * (size_t)count);
+    spans.reserve(3 * (size_t)count + 1);
     for (int i = 0; i < count; ++i) {
         auto add = [&](const void *p, int64_t bytes, bool out) { spans.push_back({(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes, out}); };
         add(A[i], 4 * shapes[i].n * shapes[i].nb, true);
         add(codes[i], 64 * tiles * shapes[i].n, false);
         add(scales[i], 4 * tiles * shapes[i].n, false);
     }
+    if (ws && need) spans.push_back({(uintptr_t)ws, (uintptr_t)ws + need, true});
     if (!apart(spans)) return DOBB_ERR_INVALID_ARG;
-    const std::vector<MomentLaunch> launches = moment_launches(count, shapes);
-    const dobb_status st = check_ws(ws, ws_bytes, moment_ws(launches, tiles));
+    const dobb_status st = check_ws(ws, ws_bytes, need);
     if (st != DOBB_OK) return st;
     for (const MomentLaunch &l : launches) {
         const void *cs[kMomentMats], *ss[kMomentMats];
@@ -275,16 +282,20 @@ dobb_status dobb_clip_grad_norm_grouped(int count, const int64_t *numel, const v
 
 dobb_status dobb_mx4_quantize(int64_t N, int64_t n, const void *X, dobb_dtype x_dtype, int64_t ldx, void *codes, void *scales,
                               dobb_stream_t stream) {
-    const dobb_status st = check_capture(N, n, X, x_dtype, ldx, codes, scales);
-    if (st != DOBB_OK) return st;
-    return hip_status(launch_mx4_quantize(N, n, X, x_dtype == DOBB_BF16, ldx, codes, scales, (hipStream_t)stream));
+    return guarded([&]() -> dobb_status {
+        const dobb_status st = check_capture(N, n, X, x_dtype, ldx, codes, scales);
+        if (st != DOBB_OK) return st;
+        return hip_status(launch_mx4_quantize(N, n, X, x_dtype == DOBB_BF16, ldx, codes, scales, (hipStream_t)stream));
+    });
 }
 
 dobb_status dobb_mx4_dequantize(int64_t N, int64_t n, const void *codes, const void *scales, void *out, dobb_dtype out_dtype,
                                 int64_t ldo, dobb_stream_t stream) {
-    const dobb_status st = check_capture(N, n, out, out_dtype, ldo, codes, scales);
-    if (st != DOBB_OK) return st;
-    return hip_status(launch_mx4_dequantize(N, n, codes, scales, out, out_dtype == DOBB_BF16, ldo, (hipStream_t)stream));
+    return guarded([&]() -> dobb_status {
+        const dobb_status st = check_capture(N, n, out, out_dtype, ldo, codes, scales);
+        if (st != DOBB_OK) return st;
+        return hip_status(launch_mx4_dequantize(N, n, codes, scales, out, out_dtype == DOBB_BF16, ldo, (hipStream_t)stream));
+    });
 }
 
 size_t dobb_moment_mx4_workspace_size(int count, const dobb_shape *shapes, int64_t tiles) {

@@ -64,7 +64,8 @@ dobb_status dobb_clip_grad_norm_grouped(int count, const int64_t *numel, const v
  * 255 and reads back as NaN.  Tokens past N are zeros.  Captures of several micro-batches with the same
  * n are joined by laying their tiles one behind the other.
  * -------------------------------------------------------------------------------------------------*/
-/* X: device, N x n (ldx >= n), fp32 or bf16, aligned to its entries only. */
+/* X: device, N x n (ldx >= n), fp32 or bf16, aligned to its entries only.  Values, codes and scales that
+ * overlap are DOBB_ERR_INVALID_ARG, here and in dobb_mx4_dequantize. */
 dobb_status dobb_mx4_quantize(int64_t N, int64_t n, const void *X, dobb_dtype x_dtype, int64_t ldx, void *codes,
                               void *scales, dobb_stream_t stream);
 /* out: device, N x n (ldo >= n), fp32 or bf16: the first N tokens' values, exact in fp32 and, from 2^-126
@@ -82,7 +83,8 @@ dobb_status dobb_accumulate_moment_mx4(const dobb_shape *s, const void *codes, c
                                        int64_t N, float beta, float *A, void *ws, size_t ws_bytes,
                                        dobb_stream_t stream);
 /* The same for a matrix set; shapes and pointer arrays are host arrays of length count.  Captures may be
- * shared by several matrices; moments that overlap each other or a capture are DOBB_ERR_INVALID_ARG. */
+ * shared by several matrices; moments or a workspace that overlap each other or a capture are
+ * DOBB_ERR_INVALID_ARG. */
 dobb_status dobb_accumulate_moment_mx4_grouped(int count, const dobb_shape *shapes, const void *const *codes,
                                                const void *const *scales, int64_t tiles, int64_t N, float beta,
                                                float *const *A, void *ws, size_t ws_bytes, dobb_stream_t stream);

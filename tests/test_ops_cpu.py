@@ -189,3 +189,36 @@ def test_optimizer_options_are_checked():
     w.grad = torch.zeros(4, 4)
     with pytest.raises(TypeError, match="GPU tensor"):
         clip_grad_norm_(w, 1.0)
+
+
+def test_captures_are_checked():
+    from block_diagonal_eigenbasis_amd.optimizer import Mx4Capture
+    codes, scales = torch.zeros(2, 4, 6, 16, dtype=torch.uint8), torch.zeros(2, 6, 4, dtype=torch.uint8)
+    assert Mx4Capture(codes, scales, (128, 100)).shape == (228, 6)
+    for c, s, parts, err in [
+        (codes, scales, (256, 1), ValueError), (codes, scales, (0, 200), ValueError), (codes, scales, (), ValueError),
+        (codes[:, :2], scales, (200,), ValueError), (codes[:, 0], scales, (200,), ValueError),
+        (codes, scales[:1], (200,), ValueError), (codes, scales[:, :5], (200,), ValueError),
+        (codes[:, :, ::2], scales[:, ::2].contiguous(), (200,), ValueError),       # strided
+        (codes[:1].expand(2, 4, 6, 16), scales, (200,), ValueError),
+        (codes, scales[:1].expand(2, 6, 4), (200,), ValueError),
+        (codes.int(), scales, (200,), TypeError), (codes, scales.to(torch.int8), (200,), TypeError),
+    ]:
+        with pytest.raises(err):
+            Mx4Capture(c, s, parts)
+
+
+def test_overlapping_captures_and_workspaces_are_refused():
+    """Everything that reaches the overlap check below breaks it, so nothing is enqueued."""
+    L = _ops._lib()
+    X, C, S, A = 0x10000000, 0x20000000, 0x30000000, 0x40000000
+    N, n, ld = 300, 40, 50                                       # 3 tiles: 7680 bytes of codes, 480 of scales
+    xb = ((N - 1) * ld + n) * 4
+    for x, c, s in [(X, X, S), (X, X + (xb // 16) * 16, S), (X, X - 7680 + 16, S), (X, C, X), (X, C, X + xb - 4),
+                    (X, C, C), (X, C, C + 7680 - 4), (X, C, C - 480 + 4)]:
+        assert L.dobb_mx4_quantize(N, n, x, 0, ld, c, s, None) == INVALID, (x, c, s)
+        assert L.dobb_mx4_dequantize(N, n, c, s, x, 0, ld, None) == INVALID, (x, c, s)
+    sh = _abi.Shape(1, 768, 192)
+    need = dobb.dobb_moment_mx4_workspace_size([(1, 768, 192)], 64)
+    for ws in (C, S, A, C - need + 256, A - need + 256, C + 64 * 64 * 768 - 256, A + 768 * 192 * 4 - 256):
+        assert L.dobb_accumulate_moment_mx4(ctypes.byref(sh), C, S, 64, 8192, 0.5, A, ws, need, None) == INVALID, ws
