@@ -39,6 +39,13 @@ class Mx4Capture:
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, parts):
         self.codes, self.scales, self.parts = codes, scales, tuple(int(k) for k in parts)
+        T, n = (codes.shape[0], codes.shape[2]) if codes.dim() == 4 else (0, 0)
+        if tuple(codes.shape) != (T, 4, n, 16) or tuple(scales.shape) != (T, n, 4):
+            raise ValueError("codes must have shape (tiles, 4, columns, 16) and scales (tiles, columns, 4)")
+        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+            raise TypeError("codes and scales must be uint8")
+        if not codes.is_contiguous() or not scales.is_contiguous() or scales.device != codes.device:
+            raise ValueError("codes and scales must be contiguous, on one device")
         if any(k < 1 for k in self.parts) or sum(_ops.mx4_tiles(k) for k in self.parts) != codes.shape[0]:
             raise ValueError("the tiles of the parts do not add up to those of the codes")
 
@@ -85,16 +92,20 @@ class Mx4Capture:
 def clip_grad_norm_(parameters, max_norm: float) -> torch.Tensor:
     """Scale the gradients of the parameters (or one parameter) in place so that their global l2 norm is at
     most max_norm, by min(1, max_norm / (norm + 1e-6)); returns the norm before, as a device scalar.
-    Gradients are contiguous, fp32 or bf16, on one device; parameters without one are passed over, and a
-    gradient shared by several counts once.  Call it over a whole model's parameters where several
-    optimizers share them (``Dobb(max_grad_norm=...)`` clips over its own)."""
+    Gradients are contiguous, fp32 or bf16, on one device; parameters without one are passed over, a
+    gradient shared by several counts once, and one that is part of another is refused.  Call it over a
+    whole model's parameters where several optimizers share them (``Dobb(max_grad_norm=...)`` clips over
+    its own)."""
     if isinstance(parameters, torch.Tensor):
         parameters = [parameters]
     grads, seen = [], set()
     for p in parameters:
         g = p.grad
-        if g is not None and (g.numel() == 0 or g.data_ptr() not in seen):
-            seen.add(g.data_ptr())
+        if g is None:
+            continue
+        key = (g.device, g.data_ptr(), g.numel(), g.dtype)
+        if g.numel() == 0 or key not in seen:
+            seen.add(key)
             grads.append(g)
     if not grads:
         return torch.zeros(())

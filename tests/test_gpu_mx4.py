@@ -79,7 +79,7 @@ def check_quantize(x):
     return codes, scales, rv
 
 
-SIZES = [(1, 1), (1, 400), (31, 3), (32, 128), (33, 129), (127, 2), (128, 127), (129, 5), (257, 130), (1000, 400), (4096, 192)]
+SIZES = [(1, 1), (300, 1), (1, 400), (31, 3), (32, 128), (33, 129), (127, 2), (128, 127), (129, 5), (257, 130), (1000, 400), (4096, 192)]
 
 
 @pytest.mark.parametrize("N,n", SIZES)

@@ -164,6 +164,19 @@ def test_clip_grad_norm_over_a_model():
     assert float(clip_grad_norm_(iter(()), 1.0)) == 0.0
 
 
+def test_clip_grad_norm_of_gradients_that_share_memory():
+    whole, part, same = (torch.nn.Parameter(torch.zeros(k, device=DEV)) for k in (12, 8, 12))
+    whole.grad = torch.full((12,), 2.0, device=DEV)
+    part.grad, same.grad = whole.grad[:8], whole.grad.view(12)
+    with pytest.raises(dobb.DobbError):
+        clip_grad_norm_([whole, part], 1.0)                      # part of the entries would be scaled twice
+    assert bool((whole.grad == 2.0).all())
+    assert abs(float(clip_grad_norm_([whole, same], 1e30)) - math.sqrt(48.0)) <= 1e-5
+    none = torch.nn.Parameter(torch.zeros(0, device=DEV))
+    none.grad = torch.zeros(0, device=DEV)
+    assert clip_grad_norm_([none], 1.0).device.type == "cuda"
+
+
 # ---- the optimizer ------------------------------------------------------------------------------------
 @pytest.mark.parametrize("basis", ["activation", "output_gradient"])
 @pytest.mark.parametrize("policy", ["first", "all"])
