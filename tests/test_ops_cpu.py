@@ -222,3 +222,21 @@ def test_overlapping_captures_and_workspaces_are_refused():
     need = dobb.dobb_moment_mx4_workspace_size([(1, 768, 192)], 64)
     for ws in (C, S, A, C - need + 256, A - need + 256, C + 64 * 64 * 768 - 256, A + 768 * 192 * 4 - 256):
         assert L.dobb_accumulate_moment_mx4(ctypes.byref(sh), C, S, 64, 8192, 0.5, A, ws, need, None) == INVALID, ws
+
+
+@pytest.mark.parametrize("n,offset", [(5, 0), (16000, 0), (16000, 2)])
+def test_captures_are_joined_whatever_their_size_and_offset(n, offset):
+    from block_diagonal_eigenbasis_amd.optimizer import Mx4Capture
+    g = torch.Generator().manual_seed(n + offset)
+
+    def held(*shape):
+        k = torch.Size(shape).numel()
+        return torch.randint(0, 256, (k + offset,), dtype=torch.uint8, generator=g)[offset:].view(shape)
+    caps = [Mx4Capture(held(t, 4, n, 16), held(t, n, 4), parts) for t, parts in ((8, (1000,)), (2, (100, 7)), (7, (896,)))]
+    got = Mx4Capture.cat(caps)
+    assert got.parts == (1000, 100, 7, 896) and got.shape == (2003, n)
+    assert got.codes.shape == (17, 4, n, 16) and got.codes.is_contiguous() and got.scales.is_contiguous()
+    at = 0
+    for c in caps:
+        assert torch.equal(got.codes[at:at + c.tiles], c.codes) and torch.equal(got.scales[at:at + c.tiles], c.scales)
+        at += c.tiles
