@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+from typing import NamedTuple
 
 import torch
 
@@ -154,9 +155,8 @@ class _Part:
         self.info = _arr([g.info[i].data_ptr() for i in self.idx])
         self.ldx = (ctypes.c_int64 * self.count)(*[c[1] for c in self.cshapes])
         self.hp = (_abi.HParams * self.count)(*[g.hp[i] for i in self.idx])
-        self.ws = None
         self.device = g.device
-        self.ensure(self.need(g, g.n_tokens))
+        self.ws = torch.empty(max(self.need(g, g.n_tokens), 256), dtype=torch.uint8, device=self.device)
 
     def need(self, g, n_tokens):
         qv = _abi.DOBB_WS_BF16_BASIS if g.q_dtype == _abi.DOBB_BF16 else 0
@@ -165,18 +165,25 @@ class _Part:
                    _abi.dobb_workspace_size(_abi.DOBB_OP_REFRESH, ash, 0, qv),
                    _abi.dobb_workspace_size(_abi.DOBB_OP_ACCUMULATE, ash, max(n_tokens, 1)))
 
-    def ensure(self, nbytes):
-        """Grow the workspace to at least nbytes.  A replaced workspace is freed in stream order (the
-        second stream's one is recorded on it)."""
-        nbytes = max(int(nbytes), 256)
-        if self.ws is None or nbytes > self.ws.numel():
-            self.ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-            if self.stream is not None:
-                self.ws.record_stream(self.stream)
+    def reserve(self, nbytes, stream):
+        """The workspace, of at least nbytes, for calls on `stream`.  A larger one is allocated in that stream's
+        order, and one that was allocated in another stream's is recorded on it: what it leaves behind is not
+        given away before every call that used it is done."""
+        if nbytes > self.ws.numel():
+            with torch.cuda.device(self.device), torch.cuda.stream(stream):
+                self.ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        self.ws.record_stream(stream)
 
     def refresh_hp(self, g):
         for k, i in enumerate(self.idx):
             self.hp[k] = g.hp[i]
+
+
+class _Plan(NamedTuple):
+    """The calls of one part that take a set of captures: lists of weights, and the bytes of workspace."""
+    mx4: list
+    dense: list
+    need: int
 
 
 class DobbGroup:
@@ -266,14 +273,17 @@ class DobbGroup:
         for part in self._parts:
             part.refresh_hp(self)
 
-    def _run(self, stream, fn):
+    def _run(self, stream, fn, plans=None):
         """fn(part, stream handle) for every part: those without a stream of their own on the caller's
-        stream, the others on theirs, forked from and joined back into the caller's stream."""
+        stream, the others on theirs, forked from and joined back into the caller's stream.  Workspaces have
+        the size of `plans` (by _plan) before the streams fork: one that grew between two calls of a part would be
+        freed while the first still runs, and another part's stream does not wait for that."""
         main = torch.cuda.current_stream(self.device) if stream is None else stream
         sides = []
         for part in self._parts:
             if part.stream is not None and part.stream not in sides:
                 sides.append(part.stream)
+            part.reserve(plans[part].need if plans else 0, main if part.stream is None else part.stream)
         for s in sides:
             s.wait_stream(main)
         for part in self._parts:
@@ -281,57 +291,58 @@ class DobbGroup:
         for s in sides:
             main.wait_stream(s)
 
-    def _grow(self, N: int) -> None:
-        if N > self.n_tokens:
-            for part in self._parts:
-                part.ensure(part.need(self, N))
-            self.n_tokens = N
-
     @staticmethod
     def _dense_tokens(xs) -> int:
         """Tokens of the longest capture given as a tensor (those in MXFP4 size their own workspace)."""
         return max((x.shape[0] for x in xs if not isinstance(x, Mx4Capture)), default=0)
 
-    def _accumulate(self, part, sh, xs, beta):
-        """One grouped capture per (activation dtype, token count), and per (tiles, token count) of those in
-        MXFP4, among the part's weights."""
-        for sub, shapes in self._mx4_groups(part, xs):
-            self._accumulate_mx4(part, sh, sub, shapes, xs, beta)
-        dense = [i for i in part.idx if not isinstance(xs[i], Mx4Capture)]
-        for sub in _split(dense, lambda i: (xs[i].dtype, xs[i].shape[0])):
-            if len(sub) == part.count:
-                ash, A, ldx = part.ash, part.A, part.ldx
-            else:
-                ash = (_abi.Shape * len(sub))(*[_abi.Shape(1, self.cap_dim(i), self.nb[i]) for i in sub])
-                A = _arr([self.A[i].data_ptr() for i in sub])
-                ldx = (ctypes.c_int64 * len(sub))(*[self.cap_dim(i) for i in sub])
-            for i in sub:
+    def _plan(self, xs):
+        """{part: its calls that take the captures xs, and the workspace they need}: one call per (tiles, token
+        count) of those in MXFP4, and per (activation dtype, token count) of the tensors.  Every capture is checked
+        here, before anything is enqueued."""
+        N = self._dense_tokens(xs)
+        plans = {}
+        for part in self._parts:
+            need = part.need(self, N) if N > self.n_tokens else 0
+            mx4 = [i for i in part.idx if isinstance(xs[i], Mx4Capture)]
+            for i in mx4:
+                if xs[i].shape[1] != self.cap_dim(i) or xs[i].device != self.device:
+                    raise ValueError(f"capture {i} must hold (tokens x {self.cap_dim(i)}) on {self.device}")
+            dense = [i for i in part.idx if not isinstance(xs[i], Mx4Capture)] if mx4 else part.idx
+            for i in dense:
                 x = xs[i]
                 if x.dim() != 2 or x.shape[1] != self.cap_dim(i) or not x.is_contiguous() or x.device != self.device:
                     raise ValueError(f"capture {i} must be a contiguous (tokens x {self.cap_dim(i)}) tensor")
-            N = xs[sub[0]].shape[0]
-            part.ensure(_abi.dobb_workspace_size(_abi.DOBB_OP_ACCUMULATE,
-                                                 [(1, self.cap_dim(i), self.nb[i]) for i in sub], N))
+            mx4 = _split(mx4, lambda i: (xs[i].tiles, xs[i].shape[0]))
+            dense = _split(dense, lambda i: (xs[i].dtype, xs[i].shape[0]))
+            for sub in mx4:
+                need = max(need, _ops.dobb_moment_mx4_workspace_size(self._cap_shapes(sub), xs[sub[0]].tiles))
+            for sub in dense:
+                need = max(need, _abi.dobb_workspace_size(_abi.DOBB_OP_ACCUMULATE, self._cap_shapes(sub), xs[sub[0]].shape[0]))
+            plans[part] = _Plan(mx4, dense, need)
+        return plans
+
+    def _cap_shapes(self, sub):
+        return [(1, self.cap_dim(i), self.nb[i]) for i in sub]
+
+    def _accumulate(self, part, plan, sh, xs, beta):
+        for sub in plan.mx4:
+            c = [xs[i] for i in sub]
+            _abi._check(_ops._lib().dobb_accumulate_moment_mx4_grouped(
+                len(sub), (_abi.Shape * len(sub))(*[_abi.Shape(*s) for s in self._cap_shapes(sub)]),
+                _arr([x.codes.data_ptr() for x in c]), _arr([x.scales.data_ptr() for x in c]), c[0].tiles, c[0].shape[0],
+                float(beta), _arr([self.A[i].data_ptr() for i in sub]), part.ws.data_ptr(), part.ws.numel(), sh),
+                "dobb_accumulate_moment_mx4_grouped")
+        for sub in plan.dense:
+            if len(sub) == part.count:
+                ash, A, ldx = part.ash, part.A, part.ldx
+            else:
+                ash = (_abi.Shape * len(sub))(*[_abi.Shape(*s) for s in self._cap_shapes(sub)])
+                A = _arr([self.A[i].data_ptr() for i in sub])
+                ldx = (ctypes.c_int64 * len(sub))(*[self.cap_dim(i) for i in sub])
             _abi._check(_abi.lib().dobb_accumulate_moment_grouped(
-                len(sub), ash, _arr([xs[i].data_ptr() for i in sub]), _abi._dtype_code(xs[sub[0]]), N, ldx,
+                len(sub), ash, _arr([xs[i].data_ptr() for i in sub]), _abi._dtype_code(xs[sub[0]]), xs[sub[0]].shape[0], ldx,
                 float(beta), A, part.ws.data_ptr(), part.ws.numel(), sh), "dobb_accumulate_moment_grouped")
-
-    def _mx4_groups(self, part, xs):
-        """(weights, their capture shapes) of every call that takes the part's captures in MXFP4."""
-        held = [i for i in part.idx if isinstance(xs[i], Mx4Capture)]
-        for i in held:
-            if xs[i].shape[1] != self.cap_dim(i) or xs[i].device != self.device:
-                raise ValueError(f"capture {i} must hold (tokens x {self.cap_dim(i)}) on {self.device}")
-        return [(sub, [(1, self.cap_dim(i), self.nb[i]) for i in sub])
-                for sub in _split(held, lambda i: (xs[i].tiles, xs[i].shape[0]))]
-
-    def _accumulate_mx4(self, part, sh, sub, shapes, xs, beta):
-        tiles, N = xs[sub[0]].tiles, xs[sub[0]].shape[0]
-        part.ensure(_ops.dobb_moment_mx4_workspace_size(shapes, tiles))
-        _abi._check(_ops._lib().dobb_accumulate_moment_mx4_grouped(
-            len(sub), (_abi.Shape * len(sub))(*[_abi.Shape(*s) for s in shapes]), _arr([xs[i].codes.data_ptr() for i in sub]),
-            _arr([xs[i].scales.data_ptr() for i in sub]), tiles, N, float(beta), _arr([self.A[i].data_ptr() for i in sub]),
-            part.ws.data_ptr(), part.ws.numel(), sh), "dobb_accumulate_moment_mx4_grouped")
 
     def _refresh(self, part, sh, mode, iters, warm_start, tol, with_lam):
         _abi._check(_abi.lib().dobb_refresh_basis_grouped(
@@ -363,8 +374,9 @@ class DobbGroup:
     def accumulate(self, xs, beta: float, stream=None) -> None:
         """Capture: A_b <- beta A_b + (1-beta)/N X_b^T X_b for every weight (xs[i] is N_i x n_i, or the
         N_i x m_i output gradients for Dobb-G), as tensors or in MXFP4."""
-        self._grow(self._dense_tokens(xs))
-        self._run(stream, lambda part, sh: self._accumulate(part, sh, xs, beta))
+        plans = self._plan(xs)
+        self._run(stream, lambda part, sh: self._accumulate(part, plans[part], sh, xs, beta), plans)
+        self.n_tokens = max(self.n_tokens, self._dense_tokens(xs))
 
     def refresh(self, mode: int, iters: int, warm_start: bool = True, tol: float = 0.0, want_lambda: bool = False,
                 stream=None) -> None:
@@ -392,17 +404,18 @@ class DobbGroup:
         """accumulate, refresh and step in one call: each part runs the three phases back to back on
         its own stream, so with streams=2 one part's refresh overlaps the other's capture and step.
         The result is the same as the three calls in turn."""
-        self._grow(self._dense_tokens(xs))
+        plans = self._plan(xs)
         G = grads if grads is not None else self.G
         if max_grad_norm is not None:
             self.clip_grads(max_grad_norm, G, stream)
         with_lam = want_lambda or mode == _abi.DOBB_REFRESH_EXACT
 
         def go(part, sh):
-            self._accumulate(part, sh, xs, beta)
+            self._accumulate(part, plans[part], sh, xs, beta)
             self._refresh(part, sh, mode, iters, warm_start, tol, with_lam)
             self._step(part, sh, G)
-        self._run(stream, go)
+        self._run(stream, go, plans)
+        self.n_tokens = max(self.n_tokens, self._dense_tokens(xs))
         self.refreshes += 1
 
     def capture_refresh_step(self, xs, beta: float, mode: int, iters: int, grads=None, warm_start: bool = True,
@@ -411,16 +424,17 @@ class DobbGroup:
         kernels on the same buffers without the per-launch host work and gaps.  xs, the gradients and
         the optimizer state are bound by address, so the caller refills them in place between replays.
         Capturing runs nothing; the workspaces must already have their size, so call refresh_step once
-        (or accumulate with the same token counts) first.  Each replay counts as one refresh."""
-        if self._dense_tokens(xs) > self.n_tokens or any(
-                part.ws.numel() < _ops.dobb_moment_mx4_workspace_size(shapes, xs[sub[0]].tiles)
-                for part in self._parts for sub, shapes in self._mx4_groups(part, xs)):
+        (or accumulate with the same token counts) first.  Each replay counts as one refresh.  The graph
+        holds the group and all tensors bound, and its workspaces, should a later call replace them: it has
+        to outlive its last replay."""
+        if self._dense_tokens(xs) > self.n_tokens or any(plan.need > part.ws.numel() for part, plan in self._plan(xs).items()):
             raise RuntimeError("call refresh_step once before capturing it (the workspaces are sized there)")
         graph = torch.cuda.CUDAGraph()
         refreshes = self.refreshes
         with torch.cuda.graph(graph):
             self.refresh_step(xs, beta, mode, iters, grads=grads, warm_start=warm_start, max_grad_norm=max_grad_norm)
         self.refreshes = refreshes
+        graph.holds = (self, xs, grads if grads is not None else self.G, [part.ws for part in self._parts])
         return graph
 
 
