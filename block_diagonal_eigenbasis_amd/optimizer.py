@@ -52,7 +52,10 @@ class Mx4Capture:
 
     @classmethod
     def quantize(cls, x: torch.Tensor) -> "Mx4Capture":
-        """(tokens x n) fp32 or bf16 -> MXFP4 (dobb_mx4_quantize)."""
+        """(tokens x n) fp32 or bf16 -> MXFP4 (dobb_mx4_quantize).  Rows of any stride are read as they are; other
+        layouts (a broadcast loss's gradient, a transposed input) are copied first."""
+        if x.dim() == 2 and (x.is_neg() or (x.shape[1] > 1 and x.stride(1) != 1) or (x.shape[0] > 1 and x.stride(0) < x.shape[1])):
+            x = x.resolve_neg().contiguous()
         codes, scales = _ops.dobb_mx4_quantize(x)
         return cls(codes, scales, (x.shape[0],))
 
@@ -504,11 +507,11 @@ class Dobb(torch.optim.Optimizer):
     def capture(self, param, x: torch.Tensor) -> None:
         """Record (tokens x n) input activations of `param` (Dobb), or (tokens x m) output gradients
         (Dobb-G), for the next refresh: the first call per refresh iteration, or every call with
-        capture="all"."""
+        capture="all".  A call without tokens is passed over."""
         x = x.detach().reshape(-1, x.shape[-1])
-        got = self._captured.setdefault(id(param), [])
-        if self.capture_policy == "all" or not got:
-            got.append(Mx4Capture.quantize(x) if self.capture_format == "mx4" else x.contiguous())
+        if x.shape[0] and (self.capture_policy == "all" or id(param) not in self._captured):
+            held = Mx4Capture.quantize(x) if self.capture_format == "mx4" else x.contiguous()
+            self._captured.setdefault(id(param), []).append(held)
 
     def attach_capture_hooks(self, modules):
         """Hooks on nn.Linear modules whose weights this optimizer owns: on refresh iterations their
