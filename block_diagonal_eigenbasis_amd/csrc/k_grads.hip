@@ -217,8 +217,10 @@ __device__ __forceinline__ void scale_chunk(const char *g, char *o, int64_t nume
 }
 
 __global__ void __launch_bounds__(kThreads) k_grad_clip(int cnt, int64_t nv, const float *total, float max_norm, ClipTable t) {
-    const float q = max_norm / (*total + 1e-6f);
-    const float c = q > 1.f ? 1.f : q;                 // a NaN stays one
+    const float norm = *total;
+    const float q = max_norm / (norm + 1e-6f);
+    // a NaN stays one, but for inf / inf: no limit on an infinite norm
+    const float c = q > 1.f || (max_norm == INFINITY && norm == INFINITY) ? 1.f : q;
     const uint32_t chunk = blockIdx.x;
     const int i = find_tensor<kClipMats>(t.first, cnt, chunk);
     const char *g = (const char *)t.g[i];

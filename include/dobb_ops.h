@@ -27,10 +27,11 @@ extern "C" {
  *   out_i[k] = G_i[k] * min(1, max_norm / (total + 1e-6))
  * G: host array of `count` device pointers to dense tensors of numel[i] entries (0 allowed, the pointer
  * may then be NULL) in g_dtypes[i] (fp32 or bf16, mixed lists allowed), aligned to their entries only.
- * The same tensor may be listed twice: it counts twice.  Squares and sums are formed in fp64, so no
- * finite fp32 gradient overflows or vanishes.  NaN and infinities propagate: a NaN makes total and
- * every clipped gradient NaN, an infinity makes total infinite and the coefficient 0 (the infinite
- * entry itself then becomes NaN).
+ * The same tensor may be listed twice: it counts twice.  Squares and sums are formed in fp64, so no square of
+ * a finite gradient overflows or vanishes; norms and total are rounded to fp32, where one above the largest
+ * fp32 value is infinite.  NaN and infinities propagate: a NaN makes total and every clipped gradient NaN; an
+ * infinite total makes the coefficient 0 (an infinite entry itself then becomes NaN), or 1 where max_norm is
+ * infinite too: no limit changes nothing.
  * norms: device fp32 [count] or NULL.  total: device fp32 scalar.
  * Clipping multiplies in fp32 and rounds to out's type once, to nearest even.  out[i] is G[i] itself
  * with the same dtype (in place: a coefficient of 1 then writes nothing) or a buffer of its own in
