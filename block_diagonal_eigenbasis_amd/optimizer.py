@@ -102,15 +102,16 @@ class Mx4Capture:
 
 def clip_grad_norm_(parameters, max_norm: float) -> torch.Tensor:
     """Scale the gradients of the parameters (or one parameter) in place so that their global l2 norm is at
-    most max_norm, by min(1, max_norm / (norm + 1e-6)); returns the norm before, as a device scalar.
+    most max_norm, by min(1, max_norm / (norm + 1e-6)); returns the norm before, as a scalar on their device.
     Gradients are contiguous, fp32 or bf16, on one device; parameters without one are passed over, a
     gradient shared by several counts once, and one that is part of another is refused.  Call it over a
     whole model's parameters where several optimizers share them (``Dobb(max_grad_norm=...)`` clips over
     its own)."""
     if isinstance(parameters, torch.Tensor):
         parameters = [parameters]
-    grads, seen = [], set()
+    grads, seen, device = [], set(), None
     for p in parameters:
+        device = device or p.device
         g = p.grad
         if g is None:
             continue
@@ -119,7 +120,7 @@ def clip_grad_norm_(parameters, max_norm: float) -> torch.Tensor:
             seen.add(key)
             grads.append(g)
     if not grads:
-        return torch.zeros(())
+        return torch.zeros((), dtype=torch.float32, device=device)
     return _ops.dobb_clip_grad_norm_grouped(grads, max_norm)
 
 
