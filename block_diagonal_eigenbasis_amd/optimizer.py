@@ -317,6 +317,7 @@ class DobbGroup:
                 x = xs[i]
                 if x.dim() != 2 or x.shape[1] != self.cap_dim(i) or not x.is_contiguous() or x.device != self.device:
                     raise ValueError(f"capture {i} must be a contiguous (tokens x {self.cap_dim(i)}) tensor")
+                _abi._dtype_code(x)
             mx4 = _split(mx4, lambda i: (xs[i].tiles, xs[i].shape[0]))
             dense = _split(dense, lambda i: (xs[i].dtype, xs[i].shape[0]))
             for sub in mx4:
@@ -354,12 +355,18 @@ class DobbGroup:
             int(iters), int(bool(warm_start)), float(tol), part.info, part.ws.data_ptr(), part.ws.numel(), sh),
             "dobb_refresh_basis_grouped")
 
+    def _checked(self, grads):
+        """The gradients of a step, checked: before anything is enqueued, and before they are clipped in place."""
+        G = grads if grads is not None else self.G
+        for i, w in enumerate(self.W):
+            g = G[i]
+            if tuple(g.shape) != tuple(w.shape) or not g.is_contiguous() or g.device != self.device:
+                raise ValueError(f"gradient {i} must be a contiguous tensor of shape {tuple(w.shape)}")
+            _abi._dtype_code(g)
+        return G
+
     def _step(self, part, sh, G):
         """One grouped step per gradient dtype among the part's weights."""
-        for i in part.idx:
-            g = G[i]
-            if tuple(g.shape) != tuple(self.W[i].shape) or not g.is_contiguous() or g.device != self.device:
-                raise ValueError(f"gradient {i} must be a contiguous tensor of shape {tuple(self.W[i].shape)}")
         for sub in _split(part.idx, lambda i: G[i].dtype):
             if len(sub) == part.count:
                 shp, Wp, Mp, Qp, hp = part.sh, part.W, part.M, part.Q, part.hp
@@ -397,7 +404,7 @@ class DobbGroup:
         return _ops.dobb_clip_grad_norm_grouped(G, max_norm, total=self.grad_norm, stream=stream)
 
     def step(self, grads=None, stream=None, max_grad_norm: float | None = None) -> None:
-        G = grads if grads is not None else self.G
+        G = self._checked(grads)
         if max_grad_norm is not None:
             self.clip_grads(max_grad_norm, G, stream)
         self._run(stream, lambda part, sh: self._step(part, sh, G))
@@ -409,7 +416,7 @@ class DobbGroup:
         its own stream, so with streams=2 one part's refresh overlaps the other's capture and step.
         The result is the same as the three calls in turn."""
         plans = self._plan(xs)
-        G = grads if grads is not None else self.G
+        G = self._checked(grads)
         if max_grad_norm is not None:
             self.clip_grads(max_grad_norm, G, stream)
         with_lam = want_lambda or mode == _abi.DOBB_REFRESH_EXACT
