@@ -290,8 +290,9 @@ class DobbGroup:
             part.reserve(plans[part].need if plans else 0, main if part.stream is None else part.stream)
         for s in sides:
             s.wait_stream(main)
-        for part in self._parts:
-            fn(part, _abi._stream(main if part.stream is None else part.stream))
+        with torch.cuda.device(self.device):
+            for part in self._parts:
+                fn(part, _abi._stream(main if part.stream is None else part.stream))
         for s in sides:
             main.wait_stream(s)
 
@@ -442,7 +443,7 @@ class DobbGroup:
             raise RuntimeError("call refresh_step once before capturing it (the workspaces are sized there)")
         graph = torch.cuda.CUDAGraph()
         refreshes = self.refreshes
-        with torch.cuda.graph(graph):
+        with torch.cuda.device(self.device), torch.cuda.graph(graph):
             self.refresh_step(xs, beta, mode, iters, grads=grads, warm_start=warm_start, max_grad_norm=max_grad_norm)
         self.refreshes = refreshes
         graph.holds = (self, xs, grads if grads is not None else self.G, [part.ws for part in self._parts])

@@ -66,6 +66,7 @@ def world(monkeypatch):
                 return getattr(self.real, name)
 
             def call(*args):
+                w.current_devices.append(w.devices[-1] if w.devices else None)
                 log.append(("call", name, args[-3], args[-1]))
                 return 0
             return call
@@ -77,7 +78,16 @@ def world(monkeypatch):
     monkeypatch.setattr(torch.cuda, "Stream", lambda *a, **k: Stream(log))
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: current[-1])
     monkeypatch.setattr(torch.cuda, "stream", on)
-    monkeypatch.setattr(torch.cuda, "device", lambda *a: contextlib.nullcontext())
+    w.devices, w.current_devices = [], []
+
+    @contextlib.contextmanager
+    def device(d):
+        w.devices.append(d)
+        try:
+            yield
+        finally:
+            w.devices.pop()
+    monkeypatch.setattr(torch.cuda, "device", device)
     monkeypatch.setattr(torch.cuda, "CUDAGraph", Graph)
     monkeypatch.setattr(torch.cuda, "graph", lambda g: on(Stream(log)))
     monkeypatch.setattr(torch.Tensor, "record_stream",
@@ -180,3 +190,15 @@ def test_a_captured_graph_keeps_its_workspaces(world, streams):
     assert all(u() is not None for u in used), "a workspace of the graph was freed"
     del graph
     assert all(u() is None for u in used)
+
+
+@pytest.mark.parametrize("streams", [1, 2])
+def test_calls_are_made_with_the_groups_device_current(world, streams):
+    g = group(DIMS, streams)
+    xs, grads = captures("mixed"), [torch.zeros(8, n) for n, _ in DIMS]
+    g.accumulate(xs, 0.9)
+    g.refresh(dobb.DOBB_REFRESH_EXACT, 0)
+    g.step(grads)
+    g.refresh_step(xs, 0.9, dobb.DOBB_REFRESH_ORTH_ITER, 1, grads)
+    g.capture_refresh_step(xs, 0.9, dobb.DOBB_REFRESH_ORTH_ITER, 1, grads)
+    assert len(world.current_devices) >= 10 and set(world.current_devices) == {g.device}
