@@ -5,7 +5,8 @@
   launch and the border inside one of them;
 * captures above 128 MB, which the narrow kernel reads past the caches;
 * more matrices of one width than a launch takes, whose launches share the workspace;
-* more gradients than a table of the norm's second kernel takes.
+* more gradients than a table of the norm's second kernel takes;
+* captures whose sums fp32 holds exactly, where the result has one rounding and no more.
 
 Tolerances of the moments: a wave runs S matrix instructions in a row, at most 64 (blocks of up to 128 columns)
 or 256; twice u = 2^-24 of the magnitudes' sum is allowed for each (one rounding of the running sum, and the
@@ -184,3 +185,38 @@ def test_quantise_ties_borders_and_subnormals_by_type(dtype):
     assert torch.equal(got.double(), value) and torch.equal(got.signbit(), neg)
     got = dobb.dobb_mx4_dequantize(codes, scales, N, BF16).cpu()
     assert torch.equal(got, value.float().to(BF16))
+
+
+# block width, blocks a matrix, matrices, tiles
+EXACT = [(1, 40, 1, 3), (16, 57, 9, 64), (32, 5, 2, 127), (33, 7, 1, 1), (64, 9, 3, 129), (100, 64, 9, 128), (100, 16, 1, 128),
+         (128, 4, 7, 32), (129, 26, 10, 32), (192, 4, 1, 32), (255, 3, 1, 5), (300, 20, 7, 32), (400, 4, 5, 400), (512, 2, 1, 128),
+         (544, 1, 1, 33), (1024, 1, 2, 128)]
+
+
+@pytest.mark.parametrize("nb,B,mats,tiles", EXACT)
+@pytest.mark.parametrize("beta", [0.0, 0.5])
+def test_sums_that_fp32_holds_are_rounded_once(nb, B, mats, tiles, beta):
+    """Columns whose groups all have one scale: products are multiples of a quarter of two scales' product, at
+    most 36 times it, so every partial sum over less than 2^24 / 144 = 116508 tokens is exact in fp32, in
+    whatever order.  What is left is the rounding of the result to fp32, half a step."""
+    print(f"exact sums: nb={nb} {mats} x {B} blocks {tiles} tiles beta={beta}", flush=True)
+    n, N = nb * B, 128 * tiles - 19
+    g = torch.Generator(device=DEV)
+    g.manual_seed(nb + tiles)
+    caps, As = [], []
+    for i in range(mats):
+        codes = torch.randint(0, 256, (tiles, 4, n, 16), generator=g, device=DEV, dtype=torch.uint8)
+        col = torch.randint(117, 138, (n,), generator=g, device=DEV, dtype=torch.uint8)
+        caps.append((codes, col.view(1, n, 1).expand(tiles, n, 4).contiguous()))
+        As.append(sym(B, nb, i) if beta else torch.full((B, nb, nb), math.nan, device=DEV))
+    A0 = [a.clone() for a in As]
+    dobb.dobb_accumulate_moment_mx4_grouped([c for c, _ in caps], [s for _, s in caps], As, [nb] * mats, N, beta)
+    for (c, s), a, a0 in zip(caps, As, A0):
+        x = dobb.dobb_mx4_dequantize(c, s, 128 * tiles)          # the tiles are full: N is the divisor alone
+        for k in range(B):
+            xb = x[:, k * nb:(k + 1) * nb].to(F64)
+            want = (1 - beta) / N * (xb.T.contiguous() @ xb)
+            if beta:
+                want += beta * a0[k].to(F64)
+            assert bool(((a[k].to(F64) - want).abs() <= U * (1 + 2.0 ** -20) * want.abs()).all()), k
+        assert torch.equal(a, a.transpose(1, 2))
