@@ -284,11 +284,12 @@ __host__ __device__ inline int wide_groups(int F) {
     return ng;
 }
 
-// GS groups of the tile pair a stage (4, or 2 where four stages of 4 would not fit the LDS); PT 16-byte
-// pieces of a stage a thread, ST scale words
-template <int GS, int PT, int ST>
+// GS groups of the tile pair a stage (4, or 2 where two stages of 4 would not fit the LDS: F > 16); PT 16-byte
+// pieces of a stage a thread, ST scale words: what GS * 64 * F pieces and 64 * F words take
+template <int GS, int PT>
 __global__ void __launch_bounds__(kWideThreads, 2) k_moment_mx4_wide(int cnt, int nb, int F, int nwg, int64_t tiles, int whole,
                                                                      int nsplit_, double beta, double scale, float *partial, MomentTable t) {
+    constexpr int ST = (PT * kWideThreads / GS + kWideThreads - 1) / kWideThreads;
     extern __shared__ __align__(16) unsigned char lds[];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int col = lane & 31, half = lane >> 5;
@@ -487,11 +488,11 @@ __global__ void __launch_bounds__(256) k_moment_mx4_reduce(int cnt, int nb, int 
 
 int wide_wgs(int64_t nb) { return (wide_groups((int)(nb + 31) / 32) + 7) / 8; }
 
-template <int GS, int PT, int ST>
+template <int GS, int PT>
 hipError_t launch_wide(const MomentMx4Args &a, const MomentTable &t, unsigned grid, int F, int nwg, double scale, hipStream_t s) {
     const size_t lds = 2 * ((size_t)GS * 1024 * F + 256 * (size_t)F);
-    (void)hipFuncSetAttribute((const void *)k_moment_mx4_wide<GS, PT, ST>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    DOBB_LAUNCH("moment_mx4_wide", s, (k_moment_mx4_wide<GS, PT, ST>), dim3(grid), dim3(kWideThreads), lds, a.count, (int)a.nb, F, nwg,
+    (void)hipFuncSetAttribute((const void *)k_moment_mx4_wide<GS, PT>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    DOBB_LAUNCH("moment_mx4_wide", s, (k_moment_mx4_wide<GS, PT>), dim3(grid), dim3(kWideThreads), lds, a.count, (int)a.nb, F, nwg,
                 a.tiles, a.plan.whole, a.plan.nsplit, (double)a.beta, scale, a.partial, t);
     return hipGetLastError();
 }
@@ -586,11 +587,22 @@ hipError_t launch_moment_mx4(const MomentMx4Args &a, hipStream_t s) {
     else if (F == 4) DOBB_MX4_NARROW(4);
 #undef DOBB_MX4_NARROW_
 #undef DOBB_MX4_NARROW
-    else if (F <= 8) e = launch_wide<4, 4, 1>(a, t, grid, F, nwg, scale, s);
-    else if (F <= 12) e = launch_wide<4, 6, 2>(a, t, grid, F, nwg, scale, s);
-    else if (F <= 14) e = launch_wide<4, 7, 2>(a, t, grid, F, nwg, scale, s);
-    else if (F <= 16) e = launch_wide<4, 8, 2>(a, t, grid, F, nwg, scale, s);
-    else e = launch_wide<2, 8, 4>(a, t, grid, F, nwg, scale, s);
+    // a stage is 64 GS F pieces: as many a thread as that takes.  Rungs for every PT against 4, 6, 7 and 8 (GS = 4)
+    // and 8 (GS = 2) alone, where threads load a piece twice: 64 blocks of 192, 16384 tokens, 37.7 and 39.1 us; 48 of
+    // 320, 67.8 and 68.7; 8 of 768, 56.3 and 61.0; the same at 400, 512 and 1024.
+#define DOBB_MX4_WIDE(GS, PT) else if (F <= 8 * (PT) / (GS)) e = launch_wide<GS, PT>(a, t, grid, F, nwg, scale, s)
+    DOBB_MX4_WIDE(4, 3);
+    DOBB_MX4_WIDE(4, 4);
+    DOBB_MX4_WIDE(4, 5);
+    DOBB_MX4_WIDE(4, 6);
+    DOBB_MX4_WIDE(4, 7);
+    DOBB_MX4_WIDE(4, 8);
+    DOBB_MX4_WIDE(2, 5);
+    DOBB_MX4_WIDE(2, 6);
+    DOBB_MX4_WIDE(2, 7);
+    DOBB_MX4_WIDE(2, 8);
+#undef DOBB_MX4_WIDE
+    else e = hipErrorInvalidValue;
     if (e == hipSuccess) e = hipGetLastError();
     if (e != hipSuccess || rest == 0) return e;
     DOBB_LAUNCH("moment_mx4_reduce", s, k_moment_mx4_reduce, dim3((unsigned)(rest * pairs)), dim3(256), 0, a.count, nb, a.plan.whole,
