@@ -3,12 +3,14 @@
 Every kernel source is compiled for gfx950 only, with packed-fp32 instructions disabled
 (-Xclang -target-feature -Xclang -packed-fp32-ops), and linked into one shared library next to this
 file; _dobb_host.so (csrc/host_ops.cpp, host code against torch's headers) is linked against it.
-build() always recompiles.
+build() always recompiles; build(host=False), or this file run with --library, makes libdobb.so alone, which needs
+hipcc but neither g++ nor torch's and Python's headers.
 """
 from __future__ import annotations
 
 import os
 import subprocess
+import sys
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -50,7 +52,7 @@ def _build_host() -> None:
     os.replace(tmp, HOST)
 
 
-def build(verbose: bool = False) -> str:
+def build(verbose: bool = False, host: bool = True) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     with ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 1)) as ex:
         objs = list(ex.map(_compile, SOURCES))
@@ -60,11 +62,14 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
-    _build_host()
+    if host:
+        _build_host()
     if verbose:
-        print(f"built {LIB} and {HOST}")
+        print(f"built {LIB} and {HOST}" if host else f"built {LIB}")
     return LIB
 
 
 if __name__ == "__main__":
-    build(verbose=True)
+    if sys.argv[1:] not in ([], ["--library"]):
+        sys.exit("usage: build.py [--library]")
+    build(verbose=True, host=not sys.argv[1:])
