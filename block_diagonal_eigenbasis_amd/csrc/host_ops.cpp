@@ -11,6 +11,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <stdexcept>
@@ -124,8 +125,8 @@ PyObject *guarded(F f) {
         PyErr_SetString(PyExc_TypeError, e.what());
     } catch (const std::invalid_argument &e) {
         PyErr_SetString(PyExc_ValueError, e.what());
-    } catch (const std::exception &e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (const std::exception &) {           // torch's own, an allocation that failed among them, under their types
+        torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }
