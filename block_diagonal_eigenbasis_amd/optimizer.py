@@ -446,7 +446,7 @@ class DobbGroup:
         with torch.cuda.device(self.device), torch.cuda.graph(graph):
             self.refresh_step(xs, beta, mode, iters, grads=grads, warm_start=warm_start, max_grad_norm=max_grad_norm)
         self.refreshes = refreshes
-        graph.holds = (self, xs, grads if grads is not None else self.G, [part.ws for part in self._parts])
+        graph.holds = (self, list(xs), list(grads if grads is not None else self.G), [part.ws for part in self._parts])
         return graph
 
 

@@ -188,8 +188,12 @@ def test_a_captured_graph_keeps_its_workspaces(world, streams):
     assert all(p.ws is not u() for p, u in zip(g._parts, used))
     g.set_streams(1)
     assert all(u() is not None for u in used), "a workspace of the graph was freed"
+    bound = [weakref.ref(t) for x in xs for t in (x.codes, x.scales)] + [weakref.ref(t) for t in grads]
+    xs.clear()
+    grads.clear()
+    assert all(b() is not None for b in bound), "a tensor that the graph reads was freed"
     del graph
-    assert all(u() is None for u in used)
+    assert all(u() is None for u in used) and all(b() is None for b in bound)
 
 
 @pytest.mark.parametrize("streams", [1, 2])
