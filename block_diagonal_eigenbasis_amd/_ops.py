@@ -141,7 +141,8 @@ def dobb_moment_mx4_workspace_size(shapes, tiles: int) -> int:
 def dobb_accumulate_moment_mx4_grouped(codes, scales, As, nbs, N: int, beta: float = 0.0, ws: torch.Tensor | None = None,
                                        stream=None) -> None:
     """As[i] (B x nb x nb fp32, symmetric) <- beta As[i] + (1 - beta)/N sum over all tiles of capture i;
-    N is the number of tokens every capture holds, and all have the same number of tiles."""
+    N is the number of tokens every capture holds, and all have the same number of tiles.  beta is rounded to
+    fp32 (0.9 to 0.9f: 1 - beta then differs by 2.4e-7 relative), as in dobb_accumulate_moment."""
     _check(_call(_host().moment_mx4, stream, codes, scales, As, nbs, N, beta, ws), "dobb_accumulate_moment_mx4_grouped")
 
 

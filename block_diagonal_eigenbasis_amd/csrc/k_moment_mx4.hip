@@ -11,15 +11,19 @@
 // k_moment_mx4_narrow (nb <= 128): a block's codes are read from HBM once, straight into operand
 //   registers.  A workgroup owns one block; its four waves take every fourth tile pair, keep all
 //   fragment pairs on or below the diagonal in registers and hand each other their sums through LDS at the
-//   end.  Bound by HBM: 576 blocks of 100, 16384 tokens (501 MB of codes), in 108 us, 5.3 TB/s with A.
+//   end.  Bound by HBM: 576 blocks of 100, 16384 tokens (501 MB of codes), in 110 us, 5.2 TB/s with A.
 // k_moment_mx4_wide (128 < nb <= 1024): a workgroup of 8 waves stages the tile pair of a whole block
 //   in LDS (through registers, one stage ahead) and each wave owns 2 x 4 of the fragment pairs on or
 //   below the diagonal; a block with more than 8 such groups takes several workgroups, neighbours on one
 //   XCD, so that its codes come from HBM once and from that XCD's L2 after that.  192 blocks of 400, 16384
-//   tokens, in 252 us; bound by the matrix cores' power: the clock falls to 1.8 GHz, and codes that are all
-//   zero take a third less time.
+//   tokens, in 280 us on average (254 at best); bound by the matrix cores' power: the clock falls to 1.8 GHz, and
+//   codes that are all zero take a third less time.
 // Rounding: fp32 sums of at most 4096 (narrow, then four of those in fp32) or 16384 tokens (wide) in
-// the accumulators, token splits in fp64 (k_moment_mx4_reduce).
+// the accumulators, token splits in fp64 (k_moment_mx4_reduce).  A product of two elements is a multiple of a
+// quarter of their scales' product and at most 36 times it, so fp32 sums of them are exact unless a column's
+// scales differ by large factors.  16384 tokens of sizes exp(0.3 N(0, 1)) and exp(N(0, 1)): every sum is exact;
+// exp(2 N(0, 1)): the diagonal is off by 4.5e-8 (root mean square; 2.8e-7 at most).  Moving the diagonal entries
+// into fp64 every four tile pairs made that 3.8e-8 (2.5e-7) and took 2 to 5 % more time: not done.
 #include <algorithm>
 
 #include "ops_internal.h"
@@ -570,8 +574,9 @@ hipError_t launch_moment_mx4(const MomentMx4Args &a, hipStream_t s) {
     const unsigned grid = (unsigned)wgs;
     hipError_t e = hipSuccess;
     // Captures larger than half of the 256 MB cache behind the L2s are read past it: what the quantising
-    // left there is gone by then (36 weights of 1600 columns, 16384 tokens, 501 MB: 124 -> 112 us); a smaller
-    // set may still be there (a 7B-style layer, 4096 tokens, 77 MB: 33 us from the cache, 36 past it).
+    // left there is gone by then (twelve GPT-2 XL layers, 16384 tokens: 403 us a call, 394 past it); a smaller set
+    // may still be there (a 7B-style layer, 4096 tokens, 77 MB, right behind its quantising: the kernel takes 25.5 us,
+    // 26.4 past it; the call on captures read before 23.2 and 26.0).
     const bool nt = blocks * a.nb * a.tiles * 68 > ((int64_t)128 << 20);
 #define DOBB_MX4_NARROW_(F, NT)                                                                                       \
     DOBB_LAUNCH("moment_mx4_narrow", s, (k_moment_mx4_narrow<F, NT>), dim3(grid), dim3(256), 0, a.count, nb, a.tiles,    \

@@ -106,7 +106,9 @@ def clip_grad_norm_(parameters, max_norm: float) -> torch.Tensor:
     Gradients are contiguous, fp32 or bf16, on one device; parameters without one are passed over, a
     gradient shared by several counts once, and one that is part of another is refused.  Call it over a
     whole model's parameters where several optimizers share them (``Dobb(max_grad_norm=...)`` clips over
-    its own)."""
+    its own).  The norm is this process's: it is the model's where every process holds all gradients, reduced.
+    Where each holds a shard, take the shards' norms (dobb_grad_norm_grouped), combine them over the
+    processes, and scale by the total (dobb_clip_grads_grouped)."""
     if isinstance(parameters, torch.Tensor):
         parameters = [parameters]
     grads, seen, device = [], set(), None
@@ -200,8 +202,8 @@ class DobbGroup:
     side="output" runs Dobb-G: block_sizes divide the output dimensions, the moments are captured from
     output gradients (accumulate takes N x m tensors) and the step is dobb_step_g.
     Captures may be tensors or ``Mx4Capture``s, mixed.  With max_grad_norm, step and refresh_step first clip
-    the gradients in place to that global norm over the set; `grad_norm` (device scalar) then holds the
-    norm before."""
+    the gradients in place to that global norm over the set, as this process holds it (``clip_grad_norm_`` says
+    what shards take instead); `grad_norm` (device scalar) then holds the norm before."""
 
     def __init__(self, weights, block_sizes, grads=None, n_tokens: int = 0, lr: float = 2.5e-3,
                  weight_decay: float = 0.0, momentum: float = 0.9, tau: float = 0.2, nesterov: bool = False,
@@ -462,11 +464,13 @@ class Dobb(torch.optim.Optimizer):
     basis="output_gradient" runs Dobb-G (Tables 12-13): blocks of rows (m // blocks, or block_size),
     bases of the output-gradient second moment, captured by the backward hooks of
     ``attach_capture_hooks`` (or ``capture(param, grad_output)``).
-    capture_format="mx4" holds captures in MXFP4 from the moment they are taken (``Mx4Capture``): about a
-    quarter of bf16's memory between the forward pass and the refresh, and of its bytes in the refresh's
-    moment; "native" keeps the tensors.  max_grad_norm clips the gradients of this optimizer's parameters
-    in place, by their global norm, before every step; ``grad_norm`` then holds the norm before (a device
-    scalar).
+    capture_format="mx4" holds captures in MXFP4 from the moment they are taken (``Mx4Capture``): 0.27 of bf16's
+    bytes an entry between the forward pass and the refresh, and in the refresh's moment; "native" keeps the
+    tensors.  Every weight's capture is quantised and held by itself, where "native" holds one tensor for all
+    weights that see it (0.41 of bf16's memory for a layer with separate q, k, v and gate, up of equal width).
+    max_grad_norm clips the gradients of this optimizer's parameters in place, by their global norm in this
+    process (``clip_grad_norm_`` says what shards take instead), before every step; ``grad_norm`` then holds the
+    norm before (a scalar on the parameters' device).
     """
 
     def __init__(self, params, lr: float = 2.5e-3, weight_decay: float = 0.0, momentum: float = 0.9,

@@ -78,7 +78,8 @@ dobb_status dobb_mx4_dequantize(int64_t N, int64_t n, const void *codes, const v
  * N is the divisor, the tokens the tiles hold (1 <= N <= 128 tiles); s->n, s->nb as for
  * dobb_accumulate_moment (n <= 2^24).  Products are formed on the matrix cores and summed in fp32 over at
  * most 16384 tokens, those sums in fp64.  A (symmetric) is
- * read when beta > 0 and the result is exactly symmetric. */
+ * read when beta > 0 and the result is exactly symmetric.  beta is a float, as in dobb_accumulate_moment, and
+ * 1 - beta is taken from it exactly: 0.9 stands for 0.9f, whose 1 - beta is 2.4e-7 relative above 0.1. */
 size_t dobb_moment_mx4_workspace_size(int count, const dobb_shape *shapes, int64_t tiles); /* 0: bad arguments, or no scratch needed */
 dobb_status dobb_accumulate_moment_mx4(const dobb_shape *s, const void *codes, const void *scales, int64_t tiles,
                                        int64_t N, float beta, float *A, void *ws, size_t ws_bytes,
