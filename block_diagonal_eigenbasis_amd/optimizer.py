@@ -246,6 +246,7 @@ class DobbGroup:
         self.norm = norm
         self.n_tokens = n_tokens
         self._parts = []
+        self._bound = []                      # workspaces that graphs captured by the caller use
         self.set_streams(streams)
         self.refreshes = 0
         self.grad_norm = torch.zeros((), dtype=torch.float32, device=dev)
@@ -285,11 +286,14 @@ class DobbGroup:
         the size of `plans` (by _plan) before the streams fork: one that grew between two calls of a part would be
         freed while the first still runs, and another part's stream does not wait for that."""
         main = torch.cuda.current_stream(self.device) if stream is None else stream
+        capturing = torch.cuda.is_current_stream_capturing()
         sides = []
         for part in self._parts:
             if part.stream is not None and part.stream not in sides:
                 sides.append(part.stream)
             part.reserve(plans[part].need if plans else 0, main if part.stream is None else part.stream)
+            if capturing and not any(w is part.ws for w in self._bound):
+                self._bound.append(part.ws)
         for s in sides:
             s.wait_stream(main)
         with torch.cuda.device(self.device):
@@ -444,10 +448,10 @@ class DobbGroup:
         if self._dense_tokens(xs) > self.n_tokens or any(plan.need > part.ws.numel() for part, plan in self._plan(xs).items()):
             raise RuntimeError("call refresh_step once before capturing it (the workspaces are sized there)")
         graph = torch.cuda.CUDAGraph()
-        refreshes = self.refreshes
+        refreshes, bound = self.refreshes, list(self._bound)
         with torch.cuda.device(self.device), torch.cuda.graph(graph):
             self.refresh_step(xs, beta, mode, iters, grads=grads, warm_start=warm_start, max_grad_norm=max_grad_norm)
-        self.refreshes = refreshes
+        self.refreshes, self._bound = refreshes, bound
         graph.holds = (self, list(xs), list(grads if grads is not None else self.G), [part.ws for part in self._parts])
         return graph
 

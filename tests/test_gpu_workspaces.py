@@ -107,3 +107,34 @@ def test_a_longer_capture_between_replays(streams):
         assert any(p.ws.data_ptr() != u for p, u in zip(a._parts, used))
         same(a, b)
     assert all(bool((j == 7.0).all()) for j in junk)
+
+
+@pytest.mark.parametrize("streams", [1, 2])
+def test_a_longer_capture_between_replays_of_the_callers_own_graph(streams):
+    print(f"the caller's own graph: {streams} streams", flush=True)
+    a, b = group(streams), roomy(streams)
+    xs = captures(TOKENS, 70)
+    longer = captures([65536, 65536, 65536, 65536], 80)
+    grads = [randn(m, n, seed=90 + i) for i, (m, n, _) in enumerate(DIMS)]
+    for g in (a, b):
+        g.refresh_step(xs, 0.0, dobb.DOBB_REFRESH_EXACT, 0, grads, warm_start=False)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.accumulate(xs, 0.9)
+        a.step(grads)
+    used = [p.ws.data_ptr() for p in a._parts]
+    junk = []
+    for it in range(4):
+        graph.replay()
+        b.accumulate(xs, 0.9)
+        b.step(grads)
+        torch.cuda.synchronize()
+        same(a, b)
+        for g in (a, b):
+            g.accumulate(longer, 0.5)
+        junk += [torch.full((1 << 20,), 7.0, device=DEV) for _ in range(16)]
+        torch.cuda.synchronize()
+        assert any(p.ws.data_ptr() != u for p, u in zip(a._parts, used))
+        same(a, b)
+    assert all(bool((j == 7.0).all()) for j in junk)

@@ -89,7 +89,16 @@ def world(monkeypatch):
             w.devices.pop()
     monkeypatch.setattr(torch.cuda, "device", device)
     monkeypatch.setattr(torch.cuda, "CUDAGraph", Graph)
-    monkeypatch.setattr(torch.cuda, "graph", lambda g: on(Stream(log)))
+    captures = []
+
+    @contextlib.contextmanager
+    def graph(g):
+        captures.append(g)
+        with on(Stream(log)):
+            yield
+        captures.pop()
+    monkeypatch.setattr(torch.cuda, "graph", graph)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: bool(captures))
     monkeypatch.setattr(torch.Tensor, "record_stream",
                         lambda t, s: log.append(("record", t.data_ptr(), s.cuda_stream)), raising=False)
     return w
@@ -206,3 +215,22 @@ def test_calls_are_made_with_the_groups_device_current(world, streams):
     g.refresh_step(xs, 0.9, dobb.DOBB_REFRESH_ORTH_ITER, 1, grads)
     g.capture_refresh_step(xs, 0.9, dobb.DOBB_REFRESH_ORTH_ITER, 1, grads)
     assert len(world.current_devices) >= 10 and set(world.current_devices) == {g.device}
+
+
+@pytest.mark.parametrize("streams", [1, 2])
+def test_a_capture_of_the_callers_own_keeps_its_workspaces(world, streams):
+    """Calls captured with torch.cuda.graph: the group cannot know how long that graph lives, and holds what it
+    was captured with for its own life."""
+    g = group(DIMS, streams)
+    xs, grads = captures("mx4"), [torch.zeros(8, n) for n, _ in DIMS]
+    g.accumulate(xs, 0.9)
+    with torch.cuda.graph(Graph()):
+        g.accumulate(xs, 0.9)
+        g.step(grads)
+    used = [weakref.ref(p.ws) for p in g._parts]
+    g.accumulate([held(n, 1 << 19) for n, _ in DIMS], 0.9)
+    assert all(p.ws is not u() for p, u in zip(g._parts, used))
+    g.set_streams(1)
+    assert all(u() is not None for u in used), "a workspace of the graph was freed"
+    del g
+    assert all(u() is None for u in used)
