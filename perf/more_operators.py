@@ -18,8 +18,8 @@ gradient, and as the capture whose second moment the basis is taken from.  The k
 * capture   micro-batches quantised as they come, then the moment from all of them.
 
 An FP8 operand holds R rows of K entries in T = ceil(K / 128) tiles: codes (T, 8, R, 16), entry
-[t][h][r] being row r's entries 128 t + 16 h on, and scales (T, R): the exponent of a tile's power of two, + 127.
-The missing entries of the last tile are zeros.  The power is the least that brings the block's largest
+[t][h][r] being row r's entries 128 t + 16 h on, and scales (T, R rounded up to fours): the exponent of a tile's
+power of two, + 127.  The missing entries of the last tile are zeros.  The power is the least that brings the block's largest
 magnitude to the format's largest value or below (2^-127 at least).
 """
 import math
@@ -282,7 +282,9 @@ def _pack(x, fmt, square):
     R, K = x.shape
     T = _tiles(K)
     v = v[:R].to(FORMATS[fmt][3]).view(torch.uint8).view(R, T, 8, 16)
-    return v.permute(1, 2, 0, 3).contiguous(), (e[:R, :, 0] + 127).to(torch.uint8).t().contiguous(), K, fmt
+    scales = torch.zeros(T, (R + 3) // 4 * 4, dtype=torch.uint8, device=x.device)
+    scales[:, :R] = (e[:R, :, 0] + 127).t()
+    return v.permute(1, 2, 0, 3).contiguous(), scales, K, fmt
 
 
 def _unpack(op):
@@ -290,7 +292,7 @@ def _unpack(op):
     codes, scales, K, fmt = op
     T, _, R, _ = codes.shape
     v = codes.permute(2, 0, 1, 3).contiguous().view(FORMATS[fmt][3]).float().view(R, T, 128)
-    return (v * _pow2(scales.t().int()[:, :, None] - 127)).view(R, T * 128)[:, :K]
+    return (v * _pow2(scales[:, :R].t().int()[:, :, None] - 127)).view(R, T * 128)[:, :K]
 
 
 def _moment(x, nb, N, beta, A):
@@ -421,7 +423,7 @@ def _operand_exact(op):
     for h in range(8):
         c = codes[:, h].permute(1, 0, 2).long()
         out[:, :, 16 * h:16 * h + 16] = torch.where(c >= 128, -1.0, 1.0).double() * lev[c & 127]
-    return (out * _two_to(scales.t().long() - 127)[:, :, None]).view(R, T * 128)[:, :K]
+    return (out * _two_to(scales[:, :R].t().long() - 127)[:, :, None]).view(R, T * 128)[:, :K]
 
 
 def _norm_exact(s):
