@@ -74,7 +74,8 @@ def _call(fn, stream, of, *args):
             got = fn(of, *args)
     if isinstance(got, tuple):
         for t in got[1:]:
-            t.record_stream(before)
+            if t is not None:
+                t.record_stream(before)
     return got
 
 

@@ -19,45 +19,20 @@
 //   tokens, in 280 us on average (254 at best); bound by the matrix cores' power: the clock falls to 1.8 GHz, and
 //   codes that are all zero take a third less time.
 // Rounding: fp32 sums of at most 4096 (narrow, then four of those in fp32) or 16384 tokens (wide) in
-// the accumulators, token splits in fp64 (k_moment_mx4_reduce).  A product of two elements is a multiple of a
+// the accumulators, token splits in fp64 (k_moment_reduce).  A product of two elements is a multiple of a
 // quarter of their scales' product and at most 36 times it, so fp32 sums of them are exact unless a column's
 // scales differ by large factors.  16384 tokens of sizes exp(0.3 N(0, 1)) and exp(N(0, 1)): every sum is exact;
 // exp(2 N(0, 1)): the diagonal is off by 4.5e-8 (root mean square; 2.8e-7 at most).  Moving the diagonal entries
 // into fp64 every four tile pairs made that 3.8e-8 (2.5e-7) and took 2 to 5 % more time: not done.
 #include <algorithm>
 
-#include "ops_internal.h"
+#include "moment_common.h"
 
 namespace dobb {
 namespace {
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-
 constexpr int kNarrow = 128;                   // widest block of the narrow kernel
 constexpr int64_t kSplitPairs = 64;            // most tile pairs of one split: 16384 tokens
-
-struct MomentTable {
-    const i32x4 *codes[kMomentMats];
-    const uint32_t *scales[kMomentMats];
-    float *A[kMomentMats];
-    int32_t n[kMomentMats];
-    int32_t first[kMomentMats + 1];            // first block of each matrix
-};
-
-// beta A + (1 - beta)/N times the sum, rounded to fp32 once
-__device__ __forceinline__ float moment_out(double beta, double scale, float A, double sum) {
-    return (float)(beta > 0.0 ? beta * (double)A + scale * sum : scale * sum);
-}
-
-__device__ __forceinline__ int find_matrix(const MomentTable &t, int cnt, int blk) {
-    int lo = 0, hi = cnt;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (t.first[mid] <= blk) lo = mid; else hi = mid;
-    }
-    return lo;
-}
 
 __device__ __forceinline__ i32x8 operand(const i32x4 &v) {
     return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0};
@@ -67,84 +42,6 @@ __device__ __forceinline__ i32x8 operand(const i32x4 &v) {
 template <int G>
 __device__ __forceinline__ f32x16 mfma_fp4(const i32x4 &a, const i32x4 &b, f32x16 c, uint32_t sa, uint32_t sb) {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(a), operand(b), c, 4, 4, G, (int)sa, G, (int)sb);
-}
-
-// Loads before it are all issued before anything behind it: the compiler otherwise tends to wait for
-// each load of a batch in turn, a memory latency apiece.
-__device__ __forceinline__ void batch() { __builtin_amdgcn_sched_barrier(0); }
-
-constexpr int kPairPad = 33;                   // row pitch of a 32x32 pair in LDS: rows and columns are read
-typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
-
-// One wave: a finished 32 x 32 pair at rows i0 and columns j0 of a block, in the accumulators' layout.
-// read_pair takes its old entries of A; store_pair writes a split's partial sums as rows of the lower
-// triangle, or the new entries of A as rows of the lower triangle and of the upper one, straight from the
-// registers: a lane's four consecutive rows are 16 contiguous bytes of the mirrored row.  A load that
-// follows a store waits for it (both count in order), so callers read for several pairs before they store
-// the first: pair by pair, an exchange with memory each, the stores were most of a short call.
-// (a block has at most 2^20 entries: 32-bit offsets from a scalar address)
-__device__ __forceinline__ float *at(const float *base, int e) { return (float *)((char *)base + (uint32_t)e * 4u); }
-
-__device__ __forceinline__ void read_pair(const float *out, int nb, int i0, int j0, float (&av)[16]) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        const int i = min(i0 + acc_row(r, lane), nb - 1), j = min(j0 + (lane & 31), i);   // no branches
-        av[r] = *at(out, i * nb + j);
-    }
-}
-
-__device__ __forceinline__ void store_pair(float *out, int nb, int i0, int j0, const f32x16 &sum, const float (&av)[16], bool part,
-                                           double beta, double scale) {
-    const int lane = threadIdx.x & 63, j = j0 + (lane & 31);
-    const bool inside = i0 + 32 <= nb && j0 < i0;                     // no bounds needed
-    const int low = i0 * nb + j;                                      // + acc_row * nb: the pair's entries
-    const int up = j * nb + i0 + 4 * (lane >> 5);                     // + 8 k: their mirrored ones, by fours
-    if (part) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-            if (inside || (i0 + acc_row(r, lane) < nb && j <= i0 + acc_row(r, lane))) *at(out, low + acc_row(r, lane) * nb) = sum[r];
-        return;
-    }
-    float w[16];
-#pragma unroll
-    for (int r = 0; r < 16; ++r) w[r] = moment_out(beta, scale, av[r], (double)sum[r]);
-    if (inside) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) *at(out, low + acc_row(r, lane) * nb) = w[r];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) *(f32x4u *)at(out, up + 8 * k) = f32x4u{w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]};
-        return;
-    }
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        const int i = i0 + acc_row(r, lane);
-        if (i < nb && j <= i) *at(out, low + acc_row(r, lane) * nb) = w[r];
-    }
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        const int i = i0 + acc_row(r, lane);
-        if (i < nb && j < i) *at(out, up + 8 * (r >> 2) + (r & 3)) = w[r];
-    }
-}
-
-// Blocks 0 .. whole - 1 of a launch take their tokens in one go, the others in nsplit splits; nwg
-// workgroups each.  The first kind come first.
-struct Place {
-    int blk, split, nsplit, wg;
-};
-__device__ __forceinline__ Place place(int whole, int nsplit, int nwg) {
-    const int w = whole * nwg;
-    Place p;
-    if ((int)blockIdx.x < w) {
-        const int id = xcd_remap(blockIdx.x, w);
-        p.wg = id % nwg; p.blk = id / nwg; p.split = 0; p.nsplit = 1;
-    } else {
-        int id = xcd_remap(blockIdx.x - w, gridDim.x - w);
-        p.wg = id % nwg; id /= nwg;
-        p.split = id % nsplit; p.blk = whole + id / nsplit; p.nsplit = nsplit;
-    }
-    return p;
 }
 
 // F = ceil(nb / 32) fragments; NT: the codes are read past the caches
@@ -442,7 +339,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) k_moment_mx4_wide(int cnt, in
 
 // The splits' sums of one 32 x 32 pair in fp64, in split order, for blocks whole .. of a launch; one
 // workgroup a pair, thread t with column t % 32 and rows t / 32 + 8 u
-__global__ void __launch_bounds__(256) k_moment_mx4_reduce(int cnt, int nb, int whole, int nsplit, int pairs, double beta,
+__global__ void __launch_bounds__(256) k_moment_reduce(int cnt, int nb, int whole, int nsplit, int pairs, double beta,
                                                            double scale, const float *partial, MomentTable t) {
     __shared__ float tile[32][kPairPad];
     const int64_t nbb = (int64_t)nb * nb;
@@ -493,7 +390,7 @@ __global__ void __launch_bounds__(256) k_moment_mx4_reduce(int cnt, int nb, int 
 int wide_wgs(int64_t nb) { return (wide_groups((int)(nb + 31) / 32) + 7) / 8; }
 
 template <int GS, int PT>
-hipError_t launch_wide(const MomentMx4Args &a, const MomentTable &t, unsigned grid, int F, int nwg, double scale, hipStream_t s) {
+hipError_t launch_wide(const MomentArgs &a, const MomentTable &t, unsigned grid, int F, int nwg, double scale, hipStream_t s) {
     const size_t lds = 2 * ((size_t)GS * 1024 * F + 256 * (size_t)F);
     (void)hipFuncSetAttribute((const void *)k_moment_mx4_wide<GS, PT>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     DOBB_LAUNCH("moment_mx4_wide", s, (k_moment_mx4_wide<GS, PT>), dim3(grid), dim3(kWideThreads), lds, a.count, (int)a.nb, F, nwg,
@@ -547,24 +444,22 @@ MomentPlan moment_mx4_plan(int64_t nb, int64_t blocks, int64_t tiles) {
     return best;
 }
 
+hipError_t launch_moment_reduce(const MomentArgs &a, const MomentTable &t, int64_t blocks, hipStream_t s) {
+    const int F = (int)(a.nb + 31) / 32, pairs = F * (F + 1) / 2;
+    DOBB_LAUNCH("moment_reduce", s, k_moment_reduce, dim3((unsigned)((blocks - a.plan.whole) * pairs)), dim3(256), 0, a.count, (int)a.nb,
+                a.plan.whole, a.plan.nsplit, pairs, (double)a.beta, (1.0 - (double)a.beta) / (double)a.N, a.partial, t);
+    return hipGetLastError();
+}
+
 size_t moment_mx4_ws(int64_t nb, int64_t blocks, int64_t tiles) {
     const MomentPlan p = moment_mx4_plan(nb, blocks, tiles);
     return (size_t)(blocks - p.whole) * (size_t)nb * (size_t)nb * 4 * (size_t)p.nsplit;
 }
 
-hipError_t launch_moment_mx4(const MomentMx4Args &a, hipStream_t s) {
+hipError_t launch_moment_mx4(const MomentArgs &a, hipStream_t s) {
     if (a.count < 1 || a.count > kMomentMats) return hipErrorInvalidValue;
-    MomentTable t{};
-    int64_t blocks = 0;
-    for (int i = 0; i < a.count; ++i) {
-        t.codes[i] = (const i32x4 *)a.codes[i];
-        t.scales[i] = (const uint32_t *)a.scales[i];
-        t.A[i] = a.A[i];
-        t.n[i] = (int32_t)a.n[i];
-        t.first[i] = (int32_t)blocks;
-        blocks += a.n[i] / a.nb;
-    }
-    t.first[a.count] = (int32_t)blocks;
+    int64_t blocks;
+    const MomentTable t = moment_table(a, &blocks);
     const int nb = (int)a.nb, F = (nb + 31) / 32;
     const int nwg = nb <= kNarrow ? 1 : wide_wgs(nb);
     const int64_t rest = blocks - a.plan.whole, pairs = (int64_t)F * (F + 1) / 2;
@@ -610,9 +505,7 @@ hipError_t launch_moment_mx4(const MomentMx4Args &a, hipStream_t s) {
     else e = hipErrorInvalidValue;
     if (e == hipSuccess) e = hipGetLastError();
     if (e != hipSuccess || rest == 0) return e;
-    DOBB_LAUNCH("moment_mx4_reduce", s, k_moment_mx4_reduce, dim3((unsigned)(rest * pairs)), dim3(256), 0, a.count, nb, a.plan.whole,
-                a.plan.nsplit, (int)pairs, (double)a.beta, scale, a.partial, t);
-    return hipGetLastError();
+    return launch_moment_reduce(a, t, blocks, s);
 }
 
 }  // namespace dobb

@@ -1,0 +1,425 @@
+// Layer norm over the columns of every row, forward and backward (formulas: dobb_layers.h).
+//
+// A row stays in the registers of the threads that read it (64 to 1024 of them, up to 16 entries each), so
+// X is read once: mean, the squares around it, and the output follow from there.  Weight, bias and, in
+// the backward pass, the sums of their gradients stay in the same threads' registers over all rows that they
+// take, and the next row is on its way while one is worked on.  Wider rows are read again for each step.
+// The mean is taken twice (the second time of what is left after the first), so that rows far from
+// zero lose nothing to its rounding.  Column sums: fp32 over a workgroup's rows, fp64 over those (k_norm_columns),
+// in a fixed order.  HBM bounds both directions.
+#include <algorithm>
+
+#include "layers_common.h"
+
+namespace dobb {
+namespace {
+
+// sum over the TPR threads of a row; `sm` holds a float a wave, twice by turns of `turn`
+template <int TPR>
+__device__ __forceinline__ float row_sum(float x, float *sm, int &turn) {
+    x = wave_sum(x);
+    if constexpr (TPR > 64) {
+        constexpr int W = TPR / 64;
+        float *s = sm + W * (turn ^= 1);
+        if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = x;
+        __syncthreads();
+        x = s[0];
+#pragma unroll
+        for (int k = 1; k < W; ++k) x += s[k];
+    }
+    return x;
+}
+
+// Rows a workgroup takes at a time, and how they go round: row group g of `groups` takes rows g, g + groups, ..
+template <int TPR>
+constexpr int kThreads = TPR == 64 ? 256 : TPR;
+template <int TPR>
+constexpr int kRowsAt = kThreads<TPR> / TPR;
+
+template <bool XB, int TPR, int CH>
+__global__ void __launch_bounds__(kThreads<TPR>) k_norm(int64_t N, int64_t n, const void *X, int64_t ldx, const void *w, const void *b,
+                                                        bool w_bf16, float eps, void *Y, bool y_bf16, int64_t ldy, float *mean_out,
+                                                        float *rstd_out) {
+    __shared__ float sm[2 * (TPR / 64)];
+    constexpr int RW = kRowsAt<TPR>;
+    const int at = threadIdx.x % TPR;
+    const int64_t stride = (int64_t)gridDim.x * RW;
+    int64_t r = (int64_t)blockIdx.x * RW + threadIdx.x / TPR;
+    int turn = 0;
+    float wv[CH][8], bv[CH][8];
+    if (Y)
+#pragma unroll
+        for (int k = 0; k < CH; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int64_t c = min<int64_t>((k * TPR + at) * 8 + j, n - 1);
+                wv[k][j] = w ? load1(w, c, w_bf16) : 1.f;
+                bv[k][j] = b ? load1(b, c, w_bf16) : 0.f;
+            }
+    Raw8<XB> raw[CH];
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int k = 0; k < CH; ++k) raw[k] = load8<XB>((const char *)X + row * ldx * (XB ? 2 : 4), (k * TPR + at) * 8, n);
+    };
+    const float inv = 1.f / (float)n;
+    if (r < N) fetch(r);
+    for (; r < N; r += stride) {
+        float x[CH][8];
+#pragma unroll
+        for (int k = 0; k < CH; ++k) unpack8<XB>(raw[k], x[k]);
+        if (r + stride < N) fetch(r + stride);
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < CH; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s += x[k][j];
+        const float m0 = row_sum<TPR>(s, sm, turn) * inv;
+        float d = 0.f, q = 0.f;                  // entries past n are zero: left out
+#pragma unroll
+        for (int k = 0; k < CH; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float u = (k * TPR + at) * 8 + j < n ? x[k][j] - m0 : 0.f;
+                d += u;
+                q = fmaf(u, u, q);
+            }
+        d = row_sum<TPR>(d, sm, turn) * inv;
+        q = row_sum<TPR>(q, sm, turn) * inv;
+        const float mean = m0 + d, rstd = 1.f / sqrtf(fmaxf(q - d * d, q * 0.f) + eps);   // (q * 0: NaN stays NaN)
+        if (at == 0) {
+            if (mean_out) mean_out[r] = mean;
+            if (rstd_out) rstd_out[r] = rstd;
+        }
+        if (Y) {
+            char *row = (char *)Y + r * ldy * (y_bf16 ? 2 : 4);
+#pragma unroll
+            for (int k = 0; k < CH; ++k) {
+                float y[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] = norm_value(x[k][j], mean, rstd, wv[k][j], bv[k][j]);
+                store8(row, (k * TPR + at) * 8, n, y, y_bf16);
+            }
+        }
+    }
+}
+
+// rows that do not fit the registers: a workgroup of 1024 a row, read three times
+template <bool XB>
+__global__ void __launch_bounds__(1024) k_norm_long(int64_t N, int64_t n, const void *X, int64_t ldx, const void *w, const void *b,
+                                                    bool w_bf16, float eps, void *Y, bool y_bf16, int64_t ldy, float *mean_out,
+                                                    float *rstd_out) {
+    __shared__ float sm[32];
+    int turn = 0;
+    const float inv = 1.f / (float)n;
+    for (int64_t r = blockIdx.x; r < N; r += gridDim.x) {
+        const char *xr = (const char *)X + r * ldx * (XB ? 2 : 4);
+        float s = 0.f, d = 0.f, q = 0.f, x[8];
+        for (int64_t c = threadIdx.x * 8; c < n; c += 8192) {
+            unpack8<XB>(load8<XB>(xr, c, n), x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s += x[j];
+        }
+        const float m0 = row_sum<1024>(s, sm, turn) * inv;
+        for (int64_t c = threadIdx.x * 8; c < n; c += 8192) {
+            unpack8<XB>(load8<XB>(xr, c, n), x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float u = c + j < n ? x[j] - m0 : 0.f;
+                d += u;
+                q = fmaf(u, u, q);
+            }
+        }
+        d = row_sum<1024>(d, sm, turn) * inv;
+        q = row_sum<1024>(q, sm, turn) * inv;
+        const float mean = m0 + d, rstd = 1.f / sqrtf(fmaxf(q - d * d, q * 0.f) + eps);
+        if (threadIdx.x == 0) {
+            if (mean_out) mean_out[r] = mean;
+            if (rstd_out) rstd_out[r] = rstd;
+        }
+        if (!Y) continue;
+        char *row = (char *)Y + r * ldy * (y_bf16 ? 2 : 4);
+        for (int64_t c = threadIdx.x * 8; c < n; c += 8192) {
+            unpack8<XB>(load8<XB>(xr, c, n), x);
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int64_t e = min<int64_t>(c + j, n - 1);
+                y[j] = norm_value(x[j], mean, rstd, w ? load1(w, e, w_bf16) : 1.f, b ? load1(b, e, w_bf16) : 0.f);
+            }
+            store8(row, c, n, y, y_bf16);
+        }
+    }
+}
+
+// ---- backward ------------------------------------------------------------------------------------
+struct GradPtrs {
+    const void *dY, *X, *w;
+    const float *mean, *rstd;
+    void *dX;
+    int64_t lddy, ldx, lddx;
+    bool w_bf16, dx_bf16;
+};
+
+template <bool DB, bool XB, int TPR, int CH>
+__global__ void __launch_bounds__(kThreads<TPR>) k_norm_grad(int64_t N, int64_t n, GradPtrs p, float *part) {
+    __shared__ float sm[2 * (TPR / 64)];
+    constexpr int RW = kRowsAt<TPR>;
+    const int at = threadIdx.x % TPR;
+    const int64_t stride = (int64_t)gridDim.x * RW;
+    int64_t r = (int64_t)blockIdx.x * RW + threadIdx.x / TPR;
+    int turn = 0;
+    float wv[CH][8], dw[CH][8], db[CH][8];
+#pragma unroll
+    for (int k = 0; k < CH; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            wv[k][j] = p.w ? load1(p.w, min<int64_t>((k * TPR + at) * 8 + j, n - 1), p.w_bf16) : 1.f;
+            dw[k][j] = db[k][j] = 0.f;
+        }
+    Raw8<XB> rx[CH];
+    Raw8<DB> rd[CH];
+    float mean = 0.f, rstd = 0.f;
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            rx[k] = load8<XB>((const char *)p.X + row * p.ldx * (XB ? 2 : 4), (k * TPR + at) * 8, n);
+            rd[k] = load8<DB>((const char *)p.dY + row * p.lddy * (DB ? 2 : 4), (k * TPR + at) * 8, n);
+        }
+    };
+    const float inv = 1.f / (float)n;
+    if (r < N) fetch(r);
+    for (; r < N; r += stride) {
+        float h[CH][8], g[CH][8];
+        mean = p.mean[r];
+        rstd = p.rstd[r];
+        float a = 0.f, c = 0.f;
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            float x[8], dy[8];
+            unpack8<XB>(rx[k], x);
+            unpack8<DB>(rd[k], dy);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {        // dy is zero past n
+                h[k][j] = (x[j] - mean) * rstd;
+                if ((k * TPR + at) * 8 + j >= n) h[k][j] = 0.f;
+                dw[k][j] = fmaf(dy[j], h[k][j], dw[k][j]);
+                db[k][j] += dy[j];
+                g[k][j] = dy[j] * wv[k][j];
+                a += g[k][j];
+                c = fmaf(g[k][j], h[k][j], c);
+            }
+        }
+        if (r + stride < N) fetch(r + stride);
+        a = row_sum<TPR>(a, sm, turn) * inv;
+        c = row_sum<TPR>(c, sm, turn) * inv;
+        char *row = (char *)p.dX + r * p.lddx * (p.dx_bf16 ? 2 : 4);
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            float dx[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dx[j] = rstd * (g[k][j] - a - h[k][j] * c);
+            store8(row, (k * TPR + at) * 8, n, dx, p.dx_bf16);
+        }
+    }
+    if (!part) return;
+    // this workgroup's sums: its rows' threads in order
+    float *out = part + (int64_t)blockIdx.x * 2 * n;
+    if constexpr (RW > 1) {
+        __shared__ float acc[RW - 1][2][8][TPR];
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            const int wr = threadIdx.x / TPR;
+            if (k > 0) __syncthreads();
+            if (wr > 0)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    acc[wr - 1][0][j][at] = dw[k][j];
+                    acc[wr - 1][1][j][at] = db[k][j];
+                }
+            __syncthreads();
+            if (wr == 0)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int q = 0; q < RW - 1; ++q) {
+                        dw[k][j] += acc[q][0][j][at];
+                        db[k][j] += acc[q][1][j][at];
+                    }
+        }
+        if (threadIdx.x >= TPR) return;
+    }
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+        store8(out, (k * TPR + at) * 8, n, dw[k], false);
+        store8(out + n, (k * TPR + at) * 8, n, db[k], false);
+    }
+}
+
+// rows that do not fit the registers: dx by rows, read twice ..
+template <bool DB, bool XB>
+__global__ void __launch_bounds__(1024) k_norm_grad_long(int64_t N, int64_t n, GradPtrs p) {
+    __shared__ float sm[32];
+    int turn = 0;
+    const float inv = 1.f / (float)n;
+    for (int64_t r = blockIdx.x; r < N; r += gridDim.x) {
+        const char *xr = (const char *)p.X + r * p.ldx * (XB ? 2 : 4), *dr = (const char *)p.dY + r * p.lddy * (DB ? 2 : 4);
+        const float mean = p.mean[r], rstd = p.rstd[r];
+        float a = 0.f, c = 0.f;
+        auto eight = [&](int64_t e, float (&g)[8], float (&h)[8]) {
+            float x[8], dy[8];
+            unpack8<XB>(load8<XB>(xr, e, n), x);
+            unpack8<DB>(load8<DB>(dr, e, n), dy);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                h[j] = e + j < n ? (x[j] - mean) * rstd : 0.f;
+                g[j] = dy[j] * (p.w ? load1(p.w, min<int64_t>(e + j, n - 1), p.w_bf16) : 1.f);
+            }
+        };
+        float g[8], h[8];
+        for (int64_t e = threadIdx.x * 8; e < n; e += 8192) {
+            eight(e, g, h);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                a += g[j];
+                c = fmaf(g[j], h[j], c);
+            }
+        }
+        a = row_sum<1024>(a, sm, turn) * inv;
+        c = row_sum<1024>(c, sm, turn) * inv;
+        char *row = (char *)p.dX + r * p.lddx * (p.dx_bf16 ? 2 : 4);
+        for (int64_t e = threadIdx.x * 8; e < n; e += 8192) {
+            eight(e, g, h);
+            float dx[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dx[j] = rstd * (g[j] - a - h[j] * c);
+            store8(row, e, n, dx, p.dx_bf16);
+        }
+    }
+}
+
+// .. and the column sums by strips of 2048 columns and groups of rows (group g takes rows g, g + groups, ..)
+template <bool DB, bool XB>
+__global__ void __launch_bounds__(256) k_norm_grad_strips(int64_t N, int64_t n, int64_t groups, GradPtrs p, float *part) {
+    const int64_t strips = (n + 2047) / 2048, g = blockIdx.x / strips;
+    const int64_t e = (blockIdx.x % strips) * 2048 + threadIdx.x * 8;
+    float dw[8] = {0.f}, db[8] = {0.f};
+    for (int64_t r = g; r < N; r += groups) {
+        float x[8], dy[8];
+        unpack8<XB>(load8<XB>((const char *)p.X + r * p.ldx * (XB ? 2 : 4), e, n), x);
+        unpack8<DB>(load8<DB>((const char *)p.dY + r * p.lddy * (DB ? 2 : 4), e, n), dy);
+        const float mean = p.mean[r], rstd = p.rstd[r];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            dw[j] = fmaf(dy[j], (x[j] - mean) * rstd, dw[j]);
+            db[j] += dy[j];
+        }
+    }
+    float *out = part + g * 2 * n;
+    store8(out, e, n, dw, false);
+    store8(out + n, e, n, db, false);
+}
+
+// the groups' sums in fp64, in order: 32 columns a workgroup, 8 threads a column
+__global__ void __launch_bounds__(256) k_norm_columns(int64_t n, int64_t groups, const float *part, void *dw, void *db, bool g_bf16) {
+    __shared__ double sm[8][32];
+    const int64_t blocks = (n + 31) / 32;
+    const bool second = blockIdx.x >= blocks;
+    const int64_t c = (blockIdx.x - (second ? blocks : 0)) * 32 + (threadIdx.x & 31);
+    const int q = threadIdx.x >> 5;
+    void *out = second ? db : dw;
+    if (!out) return;                            // (the whole workgroup)
+    const float *p = part + (second ? n : 0) + min(c, n - 1);
+    double s = 0.0;
+    int64_t g = q;
+    for (; g + 24 < groups; g += 32) {
+        float v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = p[(g + 8 * k) * 2 * n];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s += (double)v[k];
+    }
+    for (; g < groups; g += 8) s += (double)p[g * 2 * n];
+    sm[q][threadIdx.x & 31] = s;
+    __syncthreads();
+    if (q || c >= n) return;
+#pragma unroll
+    for (int k = 1; k < 8; ++k) s += sm[k][threadIdx.x];
+    if (g_bf16) ((uint16_t *)out)[c] = f32_to_bf16((float)s);
+    else ((float *)out)[c] = (float)s;
+}
+
+constexpr int64_t kInRegs = 16384;              // widest rows that stay in registers
+
+}  // namespace
+
+hipError_t launch_layer_norm(int64_t N, int64_t n, const void *X, bool x_bf16, int64_t ldx, const void *w, const void *b,
+                             bool w_bf16, float eps, void *Y, bool y_bf16, int64_t ldy, float *mean, float *rstd, hipStream_t s) {
+    if (n > kInRegs) {
+        const dim3 grid((unsigned)std::min<int64_t>(N, 512));
+        if (x_bf16) DOBB_LAUNCH("layer_norm", s, k_norm_long<true>, grid, dim3(1024), 0, N, n, X, ldx, w, b, w_bf16, eps, Y, y_bf16, ldy, mean, rstd);
+        else DOBB_LAUNCH("layer_norm", s, k_norm_long<false>, grid, dim3(1024), 0, N, n, X, ldx, w, b, w_bf16, eps, Y, y_bf16, ldy, mean, rstd);
+        return hipGetLastError();
+    }
+#define DOBB_NORM_(B, TPR, CH)                                                                                         \
+    DOBB_LAUNCH("layer_norm", s, (k_norm<B, TPR, CH>), dim3((unsigned)std::min<int64_t>((N + kRowsAt<TPR> - 1) / kRowsAt<TPR>, 1024)), \
+                dim3(kThreads<TPR>), 0, N, n, X, ldx, w, b, w_bf16, eps, Y, y_bf16, ldy, mean, rstd)
+#define DOBB_NORM(TPR, CH)                   \
+    else if (n <= 8 * (TPR) * (CH)) {        \
+        if (x_bf16) DOBB_NORM_(true, TPR, CH); \
+        else DOBB_NORM_(false, TPR, CH);     \
+    }
+    if (n < 1) return hipErrorInvalidValue;
+    DOBB_NORM(64, 1) DOBB_NORM(64, 2) DOBB_NORM(128, 2) DOBB_NORM(256, 2) DOBB_NORM(512, 2) DOBB_NORM(1024, 2)
+#undef DOBB_NORM
+#undef DOBB_NORM_
+    return hipGetLastError();
+}
+
+// Row groups of the column sums: 512 workgroups, and never more than 1024 rows for one (fp32 sums)
+int64_t norm_grad_groups(int64_t N, int64_t n) {
+    const int64_t at = n <= 1024 ? 4 : 1;
+    return std::max<int64_t>(std::min<int64_t>((N + at - 1) / at, 512), (N + 1023) / 1024);
+}
+
+hipError_t launch_layer_norm_backward(const NormGradArgs &a, hipStream_t s) {
+    const int64_t groups = norm_grad_groups(a.N, a.n), n = a.n;
+    const GradPtrs p{a.dY, a.X, a.w, a.mean, a.rstd, a.dX, a.lddy, a.ldx, a.lddx, a.w_bf16, a.dx_bf16};
+    float *part = a.dw || a.db ? a.part : nullptr;
+    if (n < 1 || groups > 0x7fffffff) return hipErrorInvalidValue;
+#define DOBB_GRAD_T(L)                                    \
+    do {                                                  \
+        if (a.dy_bf16 && a.x_bf16) { L(true, true); }     \
+        else if (a.dy_bf16) { L(true, false); }           \
+        else if (a.x_bf16) { L(false, true); }            \
+        else { L(false, false); }                         \
+    } while (0)
+#define DOBB_GRAD(TPR, CH)                                                                                                             \
+    else if (n <= 8 * (TPR) * (CH)) {                                                                                                  \
+        constexpr int T = TPR, C = CH;                                                                                                 \
+        DOBB_GRAD_T(DOBB_GRAD_L);                                                                                                      \
+    }
+#define DOBB_GRAD_L(D, B) DOBB_LAUNCH("layer_norm_grad", s, (k_norm_grad<D, B, T, C>), dim3((unsigned)groups), dim3(kThreads<T>), 0, a.N, n, p, part)
+    if (n > kInRegs) {
+        const dim3 grid((unsigned)std::min<int64_t>(a.N, 512));
+#define DOBB_GRAD_LONG(D, B) DOBB_LAUNCH("layer_norm_grad", s, (k_norm_grad_long<D, B>), grid, dim3(1024), 0, a.N, n, p)
+        DOBB_GRAD_T(DOBB_GRAD_LONG);
+        const int64_t strips = (n + 2047) / 2048;
+        if (strips > 0x7fffffff / groups) return hipErrorInvalidValue;
+#define DOBB_GRAD_STRIPS(D, B) \
+    DOBB_LAUNCH("layer_norm_grad_strips", s, (k_norm_grad_strips<D, B>), dim3((unsigned)(strips * groups)), dim3(256), 0, a.N, n, groups, p, part)
+        if (part) DOBB_GRAD_T(DOBB_GRAD_STRIPS);
+    }
+    DOBB_GRAD(64, 1) DOBB_GRAD(64, 2) DOBB_GRAD(128, 2) DOBB_GRAD(256, 2) DOBB_GRAD(512, 2) DOBB_GRAD(1024, 2)
+#undef DOBB_GRAD
+#undef DOBB_GRAD_L
+#undef DOBB_GRAD_LONG
+#undef DOBB_GRAD_STRIPS
+#undef DOBB_GRAD_T
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !part) return e;
+    const int64_t blocks = (n + 31) / 32;
+    DOBB_LAUNCH("layer_norm_columns", s, k_norm_columns, dim3((unsigned)(2 * blocks)), dim3(256), 0, n, groups, part, a.dw, a.db, a.g_bf16);
+    return hipGetLastError();
+}
+
+}  // namespace dobb

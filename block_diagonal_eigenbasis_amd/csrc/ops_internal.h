@@ -29,7 +29,7 @@ constexpr int kMomentMats = 96;       // matrices of one launch
 struct MomentPlan {
     int whole, nsplit;                // blocks 0 .. whole - 1 unsplit, the others in nsplit token splits
 };
-struct MomentMx4Args {
+struct MomentArgs {
     int count;                        // matrices with blocks of one width; at most kMomentMats
     int64_t nb, tiles, N;
     const int64_t *n;                 // columns of each matrix
@@ -42,6 +42,6 @@ struct MomentMx4Args {
 };
 MomentPlan moment_mx4_plan(int64_t nb, int64_t blocks, int64_t tiles);
 size_t moment_mx4_ws(int64_t nb, int64_t blocks, int64_t tiles);
-hipError_t launch_moment_mx4(const MomentMx4Args &a, hipStream_t s);
+hipError_t launch_moment_mx4(const MomentArgs &a, hipStream_t s);
 
 }  // namespace dobb

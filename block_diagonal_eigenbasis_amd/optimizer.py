@@ -21,7 +21,8 @@ from typing import NamedTuple
 
 import torch
 
-from . import _abi, _ops
+from . import _abi, _layers, _ops
+from ._layers import Fp8Capture
 
 
 def default_update_scale(m: int, n: int, tau: float = 0.2) -> float:
@@ -188,6 +189,7 @@ class _Part:
 class _Plan(NamedTuple):
     """The calls of one part that take a set of captures: lists of weights, and the bytes of workspace."""
     mx4: list
+    fp8: list
     dense: list
     need: int
 
@@ -201,7 +203,7 @@ class DobbGroup:
     latency-bound panel launches).  basis_dtype=torch.bfloat16 stores every Q_b in bf16.
     side="output" runs Dobb-G: block_sizes divide the output dimensions, the moments are captured from
     output gradients (accumulate takes N x m tensors) and the step is dobb_step_g.
-    Captures may be tensors or ``Mx4Capture``s, mixed.  With max_grad_norm, step and refresh_step first clip
+    Captures may be tensors, ``Mx4Capture``s or ``Fp8Capture``s, mixed.  With max_grad_norm, step and refresh_step first clip
     the gradients in place to that global norm over the set, as this process holds it (``clip_grad_norm_`` says
     what shards take instead); `grad_norm` (device scalar) then holds the norm before."""
 
@@ -304,34 +306,38 @@ class DobbGroup:
 
     @staticmethod
     def _dense_tokens(xs) -> int:
-        """Tokens of the longest capture given as a tensor (those in MXFP4 size their own workspace)."""
-        return max((x.shape[0] for x in xs if not isinstance(x, Mx4Capture)), default=0)
+        """Tokens of the longest capture given as a tensor (those in MXFP4 or FP8 size their own workspace)."""
+        return max((x.shape[0] for x in xs if not isinstance(x, (Mx4Capture, Fp8Capture))), default=0)
 
     def _plan(self, xs):
         """{part: its calls that take the captures xs, and the workspace they need}: one call per (tiles, token
-        count) of those in MXFP4, and per (activation dtype, token count) of the tensors.  Every capture is checked
-        here, before anything is enqueued."""
+        count) of those in MXFP4, per (tiles, token count, format) of those in FP8, and per (activation dtype, token
+        count) of the tensors.  Every capture is checked here, before anything is enqueued."""
         N = self._dense_tokens(xs)
         plans = {}
         for part in self._parts:
             need = part.need(self, N) if N > self.n_tokens else 0
             mx4 = [i for i in part.idx if isinstance(xs[i], Mx4Capture)]
-            for i in mx4:
+            fp8 = [i for i in part.idx if isinstance(xs[i], Fp8Capture)]
+            for i in mx4 + fp8:
                 if xs[i].shape[1] != self.cap_dim(i) or xs[i].device != self.device:
                     raise ValueError(f"capture {i} must hold (tokens x {self.cap_dim(i)}) on {self.device}")
-            dense = [i for i in part.idx if not isinstance(xs[i], Mx4Capture)] if mx4 else part.idx
+            dense = [i for i in part.idx if not isinstance(xs[i], (Mx4Capture, Fp8Capture))] if mx4 or fp8 else part.idx
             for i in dense:
                 x = xs[i]
                 if x.dim() != 2 or x.shape[1] != self.cap_dim(i) or not x.is_contiguous() or x.device != self.device:
                     raise ValueError(f"capture {i} must be a contiguous (tokens x {self.cap_dim(i)}) tensor")
                 _abi._dtype_code(x)
             mx4 = _split(mx4, lambda i: (xs[i].tiles, xs[i].shape[0]))
+            fp8 = _split(fp8, lambda i: (xs[i].tiles, xs[i].shape[0], xs[i].operand.fmt))
             dense = _split(dense, lambda i: (xs[i].dtype, xs[i].shape[0]))
             for sub in mx4:
                 need = max(need, _ops.dobb_moment_mx4_workspace_size(self._cap_shapes(sub), xs[sub[0]].tiles))
+            for sub in fp8:
+                need = max(need, _layers.dobb_moment_fp8_workspace_size(self._cap_shapes(sub), xs[sub[0]].tiles))
             for sub in dense:
                 need = max(need, _abi.dobb_workspace_size(_abi.DOBB_OP_ACCUMULATE, self._cap_shapes(sub), xs[sub[0]].shape[0]))
-            plans[part] = _Plan(mx4, dense, need)
+            plans[part] = _Plan(mx4, fp8, dense, need)
         return plans
 
     def _cap_shapes(self, sub):
@@ -345,6 +351,13 @@ class DobbGroup:
                 _arr([x.codes.data_ptr() for x in c]), _arr([x.scales.data_ptr() for x in c]), c[0].tiles, c[0].shape[0],
                 float(beta), _arr([self.A[i].data_ptr() for i in sub]), part.ws.data_ptr(), part.ws.numel(), sh),
                 "dobb_accumulate_moment_mx4_grouped")
+        for sub in plan.fp8:
+            c = [xs[i] for i in sub]
+            _abi._check(_layers._lib().dobb_accumulate_moment_fp8_grouped(
+                len(sub), (_abi.Shape * len(sub))(*[_abi.Shape(*s) for s in self._cap_shapes(sub)]),
+                (_layers._CFp8Operand * len(sub))(*[_layers._c_operand(x.operand) for x in c]), c[0].shape[0], float(beta),
+                _arr([self.A[i].data_ptr() for i in sub]), part.ws.data_ptr(), part.ws.numel(), sh),
+                "dobb_accumulate_moment_fp8_grouped")
         for sub in plan.dense:
             if len(sub) == part.count:
                 ash, A, ldx = part.ash, part.A, part.ldx
@@ -391,7 +404,7 @@ class DobbGroup:
 
     def accumulate(self, xs, beta: float, stream=None) -> None:
         """Capture: A_b <- beta A_b + (1-beta)/N X_b^T X_b for every weight (xs[i] is N_i x n_i, or the
-        N_i x m_i output gradients for Dobb-G), as tensors or in MXFP4."""
+        N_i x m_i output gradients for Dobb-G), as tensors, in MXFP4 or in FP8."""
         plans = self._plan(xs)
         self._run(stream, lambda part, sh: self._accumulate(part, plans[part], sh, xs, beta), plans)
         self.n_tokens = max(self.n_tokens, self._dense_tokens(xs))
@@ -472,6 +485,9 @@ class Dobb(torch.optim.Optimizer):
     bytes an entry between the forward pass and the refresh, and in the refresh's moment; "native" keeps the
     tensors.  Every weight's capture is quantised and held by itself, where "native" holds one tensor for all
     weights that see it (0.41 of bf16's memory for a layer with separate q, k, v and gate, up of equal width).
+    capture_format="fp8" holds them in FP8 (``Fp8Capture``; 0.50 of bf16's bytes).  ``capture`` also takes captures
+    that are held already, an ``Fp8Capture`` of the operand that the weight's gradient takes in FP8 among them: it
+    then costs neither time nor memory of its own.
     max_grad_norm clips the gradients of this optimizer's parameters in place, by their global norm in this
     process (``clip_grad_norm_`` says what shards take instead), before every step; ``grad_norm`` then holds the
     norm before (a scalar on the parameters' device).
@@ -487,8 +503,8 @@ class Dobb(torch.optim.Optimizer):
             raise ValueError('capture must be "first" or "all"')
         if basis not in ("activation", "output_gradient"):
             raise ValueError('basis must be "activation" (Dobb) or "output_gradient" (Dobb-G)')
-        if capture_format not in ("native", "mx4"):
-            raise ValueError('capture_format must be "native" or "mx4"')
+        if capture_format not in ("native", "mx4", "fp8"):
+            raise ValueError('capture_format must be "native", "mx4" or "fp8"')
         if max_grad_norm is not None and not max_grad_norm >= 0:
             raise ValueError("max_grad_norm must not be negative")
         params = [p for grp in self.param_groups for p in grp["params"]]
@@ -521,14 +537,23 @@ class Dobb(torch.optim.Optimizer):
     def wants_capture(self) -> bool:
         return self.t % self.T == 0
 
-    def capture(self, param, x: torch.Tensor) -> None:
+    def capture(self, param, x) -> None:
         """Record (tokens x n) input activations of `param` (Dobb), or (tokens x m) output gradients
         (Dobb-G), for the next refresh: the first call per refresh iteration, or every call with
-        capture="all".  A call without tokens is passed over."""
-        x = x.detach().reshape(-1, x.shape[-1])
-        if x.shape[0] and (self.capture_policy == "all" or id(param) not in self._captured):
-            held = Mx4Capture.quantize(x) if self.capture_format == "mx4" else x.contiguous()
-            self._captured.setdefault(id(param), []).append(held)
+        capture="all".  A call without tokens is passed over.  x is a tensor, or a capture that is held already (an
+        ``Mx4Capture`` or ``Fp8Capture``: kept as it is, not copied, with capture="all" for every micro-batch)."""
+        held = isinstance(x, (Mx4Capture, Fp8Capture))
+        if not held:
+            x = x.detach().reshape(-1, x.shape[-1])
+        if not x.shape[0] or (self.capture_policy != "all" and id(param) in self._captured):
+            return
+        if not held:
+            x = (Mx4Capture.quantize(x) if self.capture_format == "mx4" else
+                 Fp8Capture.quantize(x) if self.capture_format == "fp8" else x.contiguous())
+        before = self._captured.setdefault(id(param), [])
+        if before and type(before[0]) is not type(x):
+            raise ValueError(f"captures of one weight must be held alike: {type(before[0]).__name__} before, now {type(x).__name__}")
+        before.append(x)
 
     def attach_capture_hooks(self, modules):
         """Hooks on nn.Linear modules whose weights this optimizer owns: on refresh iterations their
@@ -571,7 +596,7 @@ class Dobb(torch.optim.Optimizer):
             xs = []
             for p in self._params:
                 parts = self._captured[id(p)]
-                xs.append(Mx4Capture.cat(parts) if isinstance(parts[0], Mx4Capture) else
+                xs.append(type(parts[0]).cat(parts) if isinstance(parts[0], (Mx4Capture, Fp8Capture)) else
                           parts[0] if len(parts) == 1 else torch.cat(parts, 0))
             if g.refreshes == 0:
                 g.refresh_step(xs, 0.0, _abi.DOBB_REFRESH_EXACT, 0, grads, warm_start=False)
