@@ -49,7 +49,6 @@ __device__ __forceinline__ void fp8_vm_wait() {
 }
 __device__ __forceinline__ void fp8_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 // eight codes to bf16

@@ -1,4 +1,7 @@
 // out = A B^T (+ bias) (+ out) for two FP8 operands (dobb_layers.h).
+#include <algorithm>
+#include <type_traits>
+
 #include "fp8_tile.h"
 
 namespace dobb {
@@ -10,6 +13,14 @@ struct Epilogue {
     int64_t ldo;
     bool bf16, bias_bf16, accumulate;
 };
+
+__device__ __forceinline__ void store1(const Epilogue &e, int64_t m, int64_t n, float v) {
+    if (e.bias) v += load1(e.bias, n, e.bias_bf16);
+    const int64_t at = m * e.ldo + n;
+    if (e.accumulate) v += load1(e.out, at, e.bf16);
+    if (e.bf16) ((uint16_t *)e.out)[at] = f32_to_bf16(v);
+    else ((float *)e.out)[at] = v;
+}
 
 // four neighbouring entries n .. n + 3 of row m
 __device__ __forceinline__ void store4(const Epilogue &e, int64_t m, int64_t n, int64_t N, f32x4 v) {
@@ -69,6 +80,367 @@ __global__ void __launch_bounds__(256, 2) k_fp8_matmul(Fp8Side a, Fp8Side b, int
     }
 }
 
+// ---- large products --------------------------------------------------------------------------------
+// A workgroup of four waves a CU, 256 x 256 entries at a time, a wave a quarter of them in 256 accumulators: the LDS
+// then serves 1.33 times the bytes that the matrix cores leave it time for (at 128 x 64 a wave, 0.89).  With one
+// wave a SIMD nothing else covers a wait, so everything is one stream: half tiles of k, tile after tile, go
+// through a ring of four slots; a wave's operands of the next half are read while this one is multiplied, the slot
+// that it has left is loaded again behind the barrier, three halves ahead, and a tile's results leave while the
+// next one's first slots are on their way.  The loads into LDS are written in assembly (they have no register to
+// return to): the compiler would wait for all of them before each read of LDS.
+constexpr int kBig = 256, kRing = 4;
+constexpr int kBigPieces = 2 * kBig * 64, kBigSlot = kBigPieces + 2 * kBig;
+
+__device__ __forceinline__ void dma16(const i32x4 &rsrc, uint32_t lds, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(rsrc));
+}
+__device__ __forceinline__ void dma4(const i32x4 &rsrc, uint32_t lds, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(rsrc));
+}
+__device__ __forceinline__ i32x4 buffer_of(const uint8_t *p, uint32_t bytes) {
+    const uint64_t a = (uint64_t)(uintptr_t)p;
+    return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)a), __builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xffffu)),
+                 __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
+}
+// all but the last N memory operations of this wave done (all but the last M where `more`), its LDS reads too, and
+// every wave here
+template <int N, int M>
+__device__ __forceinline__ void wait_all_but(int more) {
+    asm volatile("s_cmp_lg_u32 %2, 0\n\ts_cbranch_scc1 1f\n\ts_waitcnt vmcnt(%0)\n\ts_branch 2f\n1:\ts_waitcnt vmcnt(%1)\n2:\ts_waitcnt lgkmcnt(0)\n\ts_barrier"
+                 ::"n"(N), "n"(M), "s"(__builtin_amdgcn_readfirstlane(more)) : "memory", "scc");
+}
+template <int N>
+__device__ __forceinline__ void wait_all_but() {
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+// An accumulator's entry, fetched where it is used: the compiler moves all 256 into registers of the other kind at once,
+// more than there are, and each one that it has to fetch back from memory then waits for the stores in flight.
+__device__ __forceinline__ float acc_read(float a) {
+    float v;
+    asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a));
+    return v;
+}
+// what an instruction written in assembly has to leave between a matrix instruction and its read (19 at most)
+__device__ __forceinline__ void acc_wait() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+// keeps the order in which the source interleaves products, reads and loads
+__device__ __forceinline__ void pin() { __builtin_amdgcn_sched_barrier(0); }
+
+// Tile t of a round-robin over the chip: workgroup ids go round the XCDs, whose 32 workgroups then take
+// 32 neighbouring tiles, 8 rows of tiles by 4 columns: an XCD's L2 reads 12 strips for 32 tiles' 64.
+struct TileAt {
+    uint32_t m, n;
+};
+__device__ __forceinline__ TileAt tile_at(uint32_t t, uint32_t tm, uint32_t tn) {
+    constexpr uint32_t G = 8;
+    const uint32_t group = t / (G * tn), r = t - group * (G * tn);
+    const uint32_t rows = min(G, tm - group * G);
+    return {group * G + r % rows, r / rows};
+}
+
+using No = std::false_type;
+using Yes = std::true_type;
+
+#define DOBB_INLINE __attribute__((always_inline))
+
+struct BigArgs {
+    Fp8Side a, b;
+    uint32_t tm, tn;
+    int halves;
+    Epilogue e;
+};
+
+// A wave's results leave through a patch of LDS in rows of 128 bytes, as the L2 takes them (stored as they lie in the
+// registers, 32 bytes of 32 rows at a time: 16384 x 4800 x 1600 in 148 us instead of 139); those that are
+// added to an output in bf16 entry by entry.
+constexpr int kPatchRow = 128 + 16;              // bytes; the padding spreads rows over the banks
+constexpr int kPatch = kPatchRow / 4;
+typedef int i32x4u __attribute__((ext_vector_type(4), aligned(2)));
+
+template <int FA, int FB, bool EXACT>
+__global__ void __launch_bounds__(256, 1) k_fp8_matmul_big(BigArgs g) {
+    __shared__ __align__(16) uint8_t ring[kRing * kBigSlot];
+    __shared__ __align__(16) uint8_t patch[4][32 * kPatchRow];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 31, half = lane >> 5;
+    const uint32_t tiles = g.tm * g.tn, stride = gridDim.x;
+    const uint32_t first = (uint32_t)xcd_remap(blockIdx.x, gridDim.x);
+    const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)ring;
+    const int H = g.halves;
+
+    // the stream of loads: slot `is`, half ih of tile `it`
+    uint32_t it = first, offA[4], offB[4], offS = kFp8Off;
+    int ih = 0, is = 0;
+    const bool of_b = wave & 1;
+    const uint8_t *pa, *pb, *ps;
+    const uint32_t pitch = of_b ? g.b.pitch : g.a.pitch;
+    auto aim = [&]() DOBB_INLINE {                           // at tile `it` (past the last: at nothing)
+        const bool in = it < tiles;
+        const TileAt t = tile_at(in ? it : 0, g.tm, g.tn);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t r = t.m * kBig + 64 * k + lane, q = t.n * kBig + 64 * k + lane;
+            offA[k] = in && r < g.a.rows ? ((uint32_t)wave * g.a.rows + r) * 16 : kFp8Off;
+            offB[k] = in && q < g.b.rows ? ((uint32_t)wave * g.b.rows + q) * 16 : kFp8Off;
+        }
+        const uint32_t w = (of_b ? t.n : t.m) * kBig + 4 * lane;
+        offS = in && w < pitch ? w : kFp8Off;
+        pa = g.a.codes;
+        pb = g.b.codes;
+        ps = of_b ? g.b.scales : g.a.scales;
+    };
+    // part 0..3 of a half: a load of A, one of B (and the scales of a tile of k with its first half)
+    auto issue = [&](int part, bool scales) DOBB_INLINE {
+        const uint32_t slot = base + (uint32_t)is * kBigSlot;
+        if (scales) {
+            dma4(buffer_of(ps, pitch), slot + kBigPieces + (of_b ? kBig : 0), offS);
+            ps += pitch;
+        }
+        dma16(buffer_of(pa, 64 * g.a.rows), slot + (wave * kBig + 64 * part) * 16, offA[part]);
+        dma16(buffer_of(pb, 64 * g.b.rows), slot + kBig * 64 + (wave * kBig + 64 * part) * 16, offB[part]);
+        if (part == 3) {
+            pa += (uint64_t)64 * g.a.rows;
+            pb += (uint64_t)64 * g.b.rows;
+            is = (is + 1) & (kRing - 1);
+            ++ih;
+        }
+    };
+    auto step_tile = [&]() DOBB_INLINE {                     // before two halves
+        if (ih == H) {
+            ih = 0;
+            it += stride;
+            aim();
+        }
+    };
+
+    // a wave's operands of one half: fragments 0..3 of A, 4..7 of B
+    const int ra = (wave >> 1) * 128 + col, rb = (wave & 1) * 128 + col;
+    const uint32_t at[2] = {(uint32_t)(half * kBig + ra) * 16, (uint32_t)(kBig * 64 + (half * kBig + rb) * 16)};
+    auto read = [&](i32x8 (&f)[8], int k, int s) DOBB_INLINE {
+        const uint8_t *p = ring + s * kBigSlot + at[k >> 2] + 512 * (k & 3);
+        const i32x4 lo = *(const i32x4 *)p, hi = *(const i32x4 *)(p + 2 * kBig * 16);
+        f[k] = i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    };
+    auto read_scale = [&](uint32_t (&e)[8], int k, int s) DOBB_INLINE {
+        e[k] = ring[s * kBigSlot + kBigPieces + (k < 4 ? ra + 32 * k : kBig + rb + 32 * (k - 4))];
+    };
+    f32x16 acc[4][4];
+    i32x8 f0[8], f1[8];
+    uint32_t e0[8], e1[8];
+    int c[2][8][4];                              // EXACT: eight entries of every fragment in bf16, this step's and the next one's
+    // two of the four words: entries 8 q + 4 w .. + 3 of fragment k
+    auto convert = [&](int to, int k, int w, int src, uint32_t e) DOBB_INLINE {
+        const float scale = __uint_as_float(e << 23);
+        bf16x2 lo, hi;
+        if ((k < 4 ? FA : FB) == DOBB_E4M3) {
+            lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(src, scale, false);
+            hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(src, scale, true);
+        } else {
+            lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(src, scale, false);
+            hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(src, scale, true);
+        }
+        c[to][k][2 * w] = __builtin_bit_cast(int, lo);
+        c[to][k][2 * w + 1] = __builtin_bit_cast(int, hi);
+    };
+    auto wide = [](const int (&c)[4]) DOBB_INLINE { return __builtin_bit_cast(bf16x8, i32x4{c[0], c[1], c[2], c[3]}); };
+
+    // One half: the products of f, and between them the reads of the next half's operands (and scales, where `scales`
+    // the tile of k is the next one) and the loads of the half three ahead.
+    auto body = [&](auto fresh, const i32x8 (&f)[8], const uint32_t (&e)[8], i32x8 (&nf)[8], uint32_t (&ne)[8], auto odd, int s) DOBB_INLINE {
+        constexpr bool FRESH = decltype(fresh)::value, ODD = decltype(odd)::value;
+        const f32x16 zero{};
+        if constexpr (!EXACT) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f[4 + j], f[i], FRESH ? zero : acc[i][j], FB, FA, 0,
+                                                                                (int)e[4 + j], 0, (int)e[i]);
+                    pin();
+                    const int k = 4 * i + j;
+                    if (k < 8) read(nf, k, s);
+                    else if (k < 12) issue(k - 8, !ODD && k == 8);
+                    else if (ODD) {
+                        read_scale(ne, 2 * (k - 12), s);
+                        read_scale(ne, 2 * (k - 12) + 1, s);
+                    }
+                    pin();
+                }
+        } else {
+            auto step = [&](auto nq) DOBB_INLINE {           // entries 8 q .. + 7 of a lane, and the conversion of the next eight
+                constexpr int q = decltype(nq)::value;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wide(c[q & 1][4 + j]), wide(c[q & 1][i]), FRESH && q == 0 ? zero : acc[i][j], 0, 0, 0);
+                        pin();
+                        const int k = 4 * i + j;
+                        if constexpr (q < 3) convert((q + 1) & 1, k >> 1, k & 1, f[k >> 1][2 * (q + 1) + (k & 1)], e[k >> 1]);
+                        else if constexpr (ODD) convert(0, k >> 1, k & 1, nf[k >> 1][k & 1], ne[k >> 1]);
+                        else convert(0, k >> 1, k & 1, nf[k >> 1][k & 1], e[k >> 1]);
+                        if constexpr (q == 0) {
+                            if (k < 8) read(nf, k, s);
+                            else if (ODD && k < 12) {
+                                read_scale(ne, 2 * (k - 8), s);
+                                read_scale(ne, 2 * (k - 8) + 1, s);
+                            }
+                        } else if constexpr (q == 1) {
+                            if ((k & 3) == 0) issue(k >> 2, !ODD && k == 0);
+                        }
+                        pin();
+                    }
+            };
+            step(std::integral_constant<int, 0>());
+            step(std::integral_constant<int, 1>());
+            step(std::integral_constant<int, 2>());
+            step(std::integral_constant<int, 3>());
+        }
+    };
+
+    aim();
+#pragma unroll
+    for (int k = 0; k < kRing; ++k) {
+        if (!(k & 1)) step_tile();
+#pragma unroll
+        for (int part = 0; part < 4; ++part) issue(part, !(k & 1) && part == 0);
+    }
+    wait_all_but<25>();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        read(f0, k, 0);
+        read_scale(e0, k, 0);
+    }
+    if constexpr (EXACT)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            convert(0, k, 0, f0[k][0], e0[k]);
+            convert(0, k, 1, f0[k][1], e0[k]);
+        }
+    int s = 0;                                   // slot of the half that is multiplied
+    // Three slots of the next tile are on their way when a tile's results leave: the waits for them leave out the
+    // stores behind them (32 in bf16, 46 of the 64 in fp32, 63 being the most that a wait can leave).
+    int stored = 0;
+    constexpr int kLeft = EXACT ? 63 : 17 + 32;
+    for (uint32_t tile = first; tile < tiles; tile += stride) {
+        auto pair = [&](auto fresh) DOBB_INLINE {
+            step_tile();                         // (a branch behind the products would let the compiler move them past it)
+            wait_all_but<17, kLeft>(stored);
+            body(fresh, f0, e0, f1, e1, No(), (s + 1) & 3);
+            wait_all_but<17, kLeft>(stored);
+            body(No(), f1, e0, f0, e1, Yes(), (s + 2) & 3);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) e0[k] = e1[k];
+            s = (s + 2) & 3;
+        };
+        pair(Yes());
+        for (int h = 2; h < H; h += 2) {
+            pair(No());
+            stored = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) asm volatile("" : "+a"(acc[i][j]));   // they stay where they are
+        acc_wait();
+        const TileAt t = tile_at(tile, g.tm, g.tn);
+        const int64_t m0 = (int64_t)t.m * kBig + (wave >> 1) * 128, n0 = (int64_t)t.n * kBig + (wave & 1) * 128;
+        if (EXACT || !g.e.accumulate) {
+            // by 32 rows of 128 bytes: registers to LDS as they lie, LDS to memory in rows, 16 bytes a lane
+            constexpr int JS = EXACT ? 1 : 2, ES = EXACT ? 4 : 2;   // fragments side by side, bytes of an entry
+            const bool whole = (t.m + 1) * kBig <= g.a.rows && (t.n + 1) * kBig <= g.b.rows;
+            stored = whole && !g.e.accumulate;
+            uint8_t *mine = patch[wave];
+            uint8_t *put = mine + col * kPatchRow + (EXACT ? 16 : 8) * half;
+            const uint8_t *get = mine + (lane >> 3) * kPatchRow + (lane & 7) * 16;
+            char *out = (char *)g.e.out + ((m0 + (lane >> 3)) * g.e.ldo + n0) * ES + (lane & 7) * 16;
+            const int64_t row8 = 8 * g.e.ldo * ES;
+#pragma unroll
+            for (int j = 0; j < 4; j += JS) {
+                f32x4 bias[JS][4];
+#pragma unroll
+                for (int u = 0; u < JS; ++u)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) bias[u][q] = f32x4{};
+                if (g.e.bias)
+#pragma unroll
+                    for (int u = 0; u < JS; ++u)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int64_t n = n0 + 32 * (j + u) + 8 * q + 4 * half;
+                            if (whole && !g.e.bias_bf16) bias[u][q] = *(const f32x4u *)((const float *)g.e.bias + n);
+                            else
+#pragma unroll
+                                for (int r = 0; r < 4; ++r) bias[u][q][r] = load1(g.e.bias, min<int64_t>(n + r, (int64_t)g.b.rows - 1), g.e.bias_bf16);
+                        }
+                // this lane's columns of the output
+                const int64_t n = n0 + 32 * j + (lane & 7) * (16 / ES);
+                const int cols = n >= g.b.rows ? 0 : (int)min<int64_t>(g.b.rows - n, 16 / ES);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                    for (int u = 0; u < JS; ++u)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const f32x16 &c = acc[i][j + u];
+                            const f32x4 v = f32x4{acc_read(c[4 * q]), acc_read(c[4 * q + 1]), acc_read(c[4 * q + 2]), acc_read(c[4 * q + 3])} + bias[u][q];
+                            if constexpr (EXACT) *(f32x4 *)(put + 32 * q) = v;
+                            else *(uint2 *)(put + 64 * u + 16 * q) = uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+                        }
+                    pin();
+                    i32x4 w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) w[k] = *(const i32x4 *)(get + 8 * k * kPatchRow);
+                    char *o = out + 4 * i * row8 + 128 * (j / JS);
+                    if (stored) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) *(i32x4u *)(o + k * row8) = w[k];
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (m0 + 32 * i + 8 * k + (lane >> 3) >= g.a.rows) continue;
+                            char *at = o + k * row8;
+                            if constexpr (EXACT) {
+                                f32x4 v = __builtin_bit_cast(f32x4, w[k]);
+                                if (cols == 4) {
+                                    if (g.e.accumulate) v += *(const f32x4u *)at;
+                                    *(f32x4u *)at = v;
+                                } else
+#pragma unroll
+                                    for (int r = 0; r < 3; ++r)
+                                        if (r < cols) ((float *)at)[r] = g.e.accumulate ? v[r] + ((float *)at)[r] : v[r];
+                            } else if (cols == 8) *(i32x4u *)at = w[k];
+                            else
+#pragma unroll
+                                for (int r = 0; r < 7; ++r)
+                                    if (r < cols) ((uint16_t *)at)[r] = (uint16_t)((uint32_t)w[k][r >> 1] >> (16 * (r & 1)));
+                        }
+                    }
+                    pin();
+                }
+            }
+        } else {
+            stored = 0;
+            float *mine = (float *)patch[wave];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (m0 + 32 * i >= g.a.rows || n0 + 32 * j >= g.b.rows) continue;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) mine[col * kPatch + acc_row(r, lane)] = acc_read(acc[i][j][r]);
+                    __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+                    for (int r = 0; r < 16; ++r) {
+                        const int64_t m = m0 + 32 * i + 2 * r + half, n = n0 + 32 * j + col;
+                        if (m < g.a.rows && n < g.b.rows) store1(g.e, m, n, mine[(2 * r + half) * kPatch + col]);
+                    }
+                    __builtin_amdgcn_wave_barrier();
+                }
+        }
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
 }  // namespace
 
 size_t fp8_matmul_ws(int64_t M, int64_t N, int64_t k) { return 0; }
@@ -99,6 +471,22 @@ hipError_t launch_fp8_matmul(const dobb_fp8_operand &A, const dobb_fp8_operand &
         else if (B.format == DOBB_E4M3) DOBB_FP8_MM(TM, TN, 1, 0);                            \
         else DOBB_FP8_MM(TM, TN, 1, 1);                                                       \
     } while (0)
+    const int64_t tm = (A.rows + kBig - 1) / kBig, tn = (B.rows + kBig - 1) / kBig;
+    if (tm * tn >= 64 && tm * tn < 0x7fffffff - 256 && halves <= 0x7ffffff0) {
+        const BigArgs g{a, b, (uint32_t)tm, (uint32_t)tn, (int)halves, e};
+        const dim3 grid((unsigned)std::min<int64_t>(tm * tn, 256));
+#define DOBB_FP8_BIG(FA, FB)                                                                                            \
+    do {                                                                                                               \
+        if (out_bf16) DOBB_LAUNCH("fp8_matmul", s, (k_fp8_matmul_big<FA, FB, false>), grid, dim3(256), 0, g);          \
+        else DOBB_LAUNCH("fp8_matmul", s, (k_fp8_matmul_big<FA, FB, true>), grid, dim3(256), 0, g);                    \
+    } while (0)
+        if (A.format == DOBB_E4M3 && B.format == DOBB_E4M3) DOBB_FP8_BIG(0, 0);
+        else if (A.format == DOBB_E4M3) DOBB_FP8_BIG(0, 1);
+        else if (B.format == DOBB_E4M3) DOBB_FP8_BIG(1, 0);
+        else DOBB_FP8_BIG(1, 1);
+#undef DOBB_FP8_BIG
+        return hipGetLastError();
+    }
     if (A.rows <= 128) DOBB_FP8_MM_F(128, 128);
     else DOBB_FP8_MM_F(256, 128);
 #undef DOBB_FP8_MM_F

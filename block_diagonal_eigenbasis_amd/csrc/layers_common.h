@@ -48,7 +48,9 @@ __device__ __forceinline__ Raw8<BF16> load8(const void *row, int64_t c, int64_t 
     return r;
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) { return (uint32_t)f32_to_bf16(a) | ((uint32_t)f32_to_bf16(b) << 16); }
+// to nearest, ties to even (v_cvt_pk_bf16_f32)
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) { return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b}); }
 
 __device__ __forceinline__ void store8(void *row, int64_t c, int64_t n, const float (&v)[8], bool bf16) {
     if (bf16) {

@@ -155,6 +155,36 @@ def test_matmul(M, N, K, dtype):
     check_matmul(operand(M, K, M + K), operand(N, K, N + 2 * K, square=True), dtype)
 
 
+# many tiles of 256 x 256: one tile of k, an odd and an even number; more tiles than workgroups; edges on either side, none
+@pytest.mark.parametrize("M,N,K", [(2100, 2300, 100), (2048, 2048, 256), (2049, 2047, 257), (4200, 4500, 130), (300, 16400, 384),
+                                   (16500, 250, 500), (4096, 4352, 640)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_matmul_many_tiles(M, N, K, dtype):
+    check_matmul(operand(M, K, M + K), operand(N, K, N + 2 * K, square=True), dtype)
+
+
+@pytest.mark.parametrize("fa,fb", [("e5m2", "e4m3"), ("e4m3", "e5m2"), ("e5m2", "e5m2")])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_matmul_many_tiles_bias_accumulate(fa, fb, dtype):
+    M, N, K = 2060, 2310, 300
+    a, b = operand(M, K, 1, fa), operand(N, K, 2, fb)
+    g = torch.Generator()
+    g.manual_seed(3)
+    bias = torch.randn(N, generator=g)
+    check_matmul(a, b, dtype, bias=bias.to(DEV))
+    check_matmul(a, b, dtype, bias=bias.to(BF16).to(DEV))
+    old = torch.randn(M, N, generator=g).to(dtype).to(DEV)
+    check_matmul(a, b, dtype, out=old.clone(), accumulate=True)
+    check_matmul(a, b, dtype, out=old.clone(), accumulate=True, bias=bias.to(DEV))
+    big = torch.full((M, N + 23), 5.0, dtype=dtype, device=DEV)
+    got = check_matmul(a, b, dtype, out=big[:, 11:11 + N], bias=bias.to(DEV))
+    assert got.data_ptr() == big[:, 11:].data_ptr()
+    assert bool((big[:, :11] == 5.0).all()) and bool((big[:, 11 + N:] == 5.0).all())
+    first = dobb.dobb_fp8_matmul(a, b, dtype=dtype)
+    for _ in range(5):
+        assert torch.equal(first, dobb.dobb_fp8_matmul(a, b, dtype=dtype))
+
+
 @pytest.mark.parametrize("fa", ["e4m3", "e5m2"])
 @pytest.mark.parametrize("fb", ["e4m3", "e5m2"])
 @pytest.mark.parametrize("M", [3, 90, 400])
@@ -175,7 +205,7 @@ def test_matmul_formats_bias_accumulate(fa, fb, M):
         assert torch.equal(got, dobb.dobb_fp8_matmul(a, b, dtype=dtype))
 
 
-@pytest.mark.parametrize("M,N", [(2, 40), (200, 300)])
+@pytest.mark.parametrize("M,N", [(2, 40), (200, 300), (2050, 2060)])
 def test_matmul_not_finite_and_wide_scales(M, N):
     """A block that is not finite makes its row NaN and no other; scales far apart keep every row's precision."""
     x = values(M, 300, 1)
