@@ -44,8 +44,8 @@ __device__ __forceinline__ void lds_load4(__amdgpu_buffer_rsrc_t r, void *dst, u
 }
 template <int N>
 __device__ __forceinline__ void fp8_vm_wait() {
-    static_assert(N >= 0 && N < 16, "vmcnt immediate");
-    __builtin_amdgcn_s_waitcnt(0x0f70 | N);
+    static_assert(N >= 0 && N < 64, "vmcnt immediate");
+    __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));
 }
 __device__ __forceinline__ void fp8_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 

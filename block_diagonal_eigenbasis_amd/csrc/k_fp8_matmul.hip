@@ -1,5 +1,6 @@
 // out = A B^T (+ bias) (+ out) for two FP8 operands (dobb_layers.h).
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "fp8_tile.h"
@@ -51,22 +52,30 @@ __device__ __forceinline__ void store4(const Epilogue &e, int64_t m, int64_t n, 
             if (n + k < N) ((float *)o)[k] = v[k];
 }
 
-template <int TM, int TN, int FA, int FB, bool EXACT>
-__global__ void __launch_bounds__(256, 2) k_fp8_matmul(Fp8Side a, Fp8Side b, int64_t halves, int tilesN, Epilogue e) {
-    using T = Fp8Tile<TM, TN, 3, FA, FB, EXACT>;
-    __shared__ __align__(16) uint8_t b0[T::kSlot], b1[T::kSlot], b2[T::kSlot];
-    uint8_t *const bufs[3] = {b0, b1, b2};
+// ---- few tiles -------------------------------------------------------------------------------------
+// TM x TN entries a workgroup, over one of nsplit parts of k: the result, or with more than one part a partial
+// product (parts x M x N in fp32) for k_fp8_join.
+template <int TM, int TN, int NS, int FA, int FB, bool EXACT>
+__global__ void __launch_bounds__(256, 2) k_fp8_matmul(Fp8Side a, Fp8Side b, int64_t tiles, int tilesN, int nsplit, Epilogue e, float *part) {
+    using T = Fp8Tile<TM, TN, NS, FA, FB, EXACT>;
+    __shared__ __align__(16) uint8_t ring[NS][T::kSlot];
+    uint8_t *bufs[NS];
+#pragma unroll
+    for (int k = 0; k < NS; ++k) bufs[k] = ring[k];
     const int id = xcd_remap(blockIdx.x, gridDim.x);
-    a.row0 = (uint32_t)(id / tilesN) * TM;
-    b.row0 = (uint32_t)(id % tilesN) * TN;
+    const int split = id % nsplit, tile = id / nsplit;
+    const int64_t per = (tiles + nsplit - 1) / nsplit, t0 = per * split, t1 = min(t0 + per, tiles);
+    a.row0 = (uint32_t)(tile / tilesN) * TM;
+    b.row0 = (uint32_t)(tile % tilesN) * TN;
     const T t(a, b);
     f32x16 acc[T::kFM][T::kFN];
 #pragma unroll
     for (int i = 0; i < T::kFM; ++i)
 #pragma unroll
         for (int j = 0; j < T::kFN; ++j) acc[i][j] = f32x16{};
-    t.run(0, halves, bufs, acc);
+    t.run(2 * t0, 2 * t1, bufs, acc);
     const int lane = threadIdx.x & 63;
+    if (nsplit > 1) e = Epilogue{part + (int64_t)split * a.rows * b.rows, nullptr, (int64_t)b.rows, false, false, false};
 #pragma unroll
     for (int i = 0; i < T::kFM; ++i) {
         const int64_t m = a.row0 + (t.wave >> 1) * T::kWM + 32 * i + (lane & 31);
@@ -77,6 +86,86 @@ __global__ void __launch_bounds__(256, 2) k_fp8_matmul(Fp8Side a, Fp8Side b, int
             for (int q = 0; q < 4; ++q)
                 store4(e, m, (int64_t)b.row0 + (t.wave & 1) * T::kWN + 32 * j + 8 * q + 4 * (lane >> 5), b.rows,
                        f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]});
+    }
+}
+
+// the parts' sums, in order, four neighbouring entries a thread
+__global__ void __launch_bounds__(256) k_fp8_join(int64_t M, int64_t N, int nsplit, const float *part, Epilogue e) {
+    const int64_t quads = (N + 3) / 4, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (at >= M * quads) return;
+    const int64_t m = at / quads, n = at % quads * 4;
+    const float *p = part + m * N + n;
+    f32x4 s{};
+    if (n + 4 <= N) {
+        for (int k = 0; k < nsplit; ++k) s += *(const f32x4u *)(p + k * M * N);
+    } else
+#pragma unroll
+        for (int r = 0; r < 3; ++r)
+            if (n + r < N)
+                for (int k = 0; k < nsplit; ++k) s[r] += p[k * M * N + r];
+    store4(e, m, n, N, s);
+}
+
+// ---- few rows --------------------------------------------------------------------------------------
+// An operand b of many rows against one, a, of at most 32: b is read once, straight into the instruction's
+// registers.  A workgroup takes 32 rows of b, its W waves every W-th tile of k, some tiles' loads in flight, and adds
+// their sums up in the order of the waves through LDS.  `turned`: b is the product's A, so the output is transposed.
+template <int FA, int FB, bool EXACT>
+__global__ void __launch_bounds__(256) k_fp8_matmul_thin(Fp8Side a, Fp8Side b, int64_t tiles, bool turned, Epilogue e) {
+    constexpr int kAhead = 4;
+    extern __shared__ float sums[];              // W x 32 x 32
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W = blockDim.x >> 6;
+    const int col = lane & 31, half = lane >> 5;
+    const uint32_t n0 = (uint32_t)xcd_remap(blockIdx.x, gridDim.x) * 32;
+    const uint32_t rb = min(n0 + col, b.rows - 1), ra = min((uint32_t)col, a.rows - 1);
+    f32x16 acc{};
+    for (int64_t t = wave; t < tiles; t += kAhead * W) {
+        i32x4 x[kAhead][4], y[kAhead][4];        // a half-wave's pieces of a tile: every other one
+        uint32_t ea[kAhead], eb[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t tt = min(t + k * W, tiles - 1);
+            const i32x4 *pa = (const i32x4 *)a.codes + (tt * 8 + half) * a.rows + ra, *pb = (const i32x4 *)b.codes + (tt * 8 + half) * b.rows + rb;
+            ea[k] = a.scales[tt * a.pitch + ra];
+            eb[k] = b.scales[tt * b.pitch + rb];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                y[k][h] = pb[(uint64_t)(2 * h) * b.rows];
+                x[k][h] = pa[(uint64_t)(2 * h) * a.rows];
+            }
+        }
+        batch();
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (t + k * W >= tiles) break;
+#pragma unroll
+            for (int h = 0; h < 4; h += 2) {
+                if constexpr (EXACT) {
+                    const float fa = __uint_as_float(ea[k] << 23), fb = __uint_as_float(eb[k] << 23);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const i32x4 &p = x[k][h + (u >> 1)], &q = y[k][h + (u >> 1)];
+                        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fp8_to_bf16<FB>(q[2 * (u & 1)], q[2 * (u & 1) + 1], fb),
+                                                                     fp8_to_bf16<FA>(p[2 * (u & 1)], p[2 * (u & 1) + 1], fa), acc, 0, 0, 0);
+                    }
+                } else {
+                    const i32x4 &p0 = x[k][h], &p1 = x[k][h + 1], &q0 = y[k][h], &q1 = y[k][h + 1];
+                    acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(i32x8{q0[0], q0[1], q0[2], q0[3], q1[0], q1[1], q1[2], q1[3]},
+                                                                          i32x8{p0[0], p0[1], p0[2], p0[3], p1[0], p1[1], p1[2], p1[3]}, acc, FB, FA, 0,
+                                                                          (int)eb[k], 0, (int)ea[k]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)                  // [wave][row of a][row of b]
+        *(f32x4 *)(sums + (wave * 32 + col) * 32 + 8 * q + 4 * half) = f32x4{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
+    __syncthreads();
+    for (uint32_t at = threadIdx.x; at < 32 * a.rows; at += blockDim.x) {
+        float s = sums[at];
+        for (int w = 1; w < W; ++w) s += sums[w * 1024 + at];
+        const uint32_t m = at >> 5, n = n0 + (at & 31);
+        if (n < b.rows) store1(e, turned ? n : m, turned ? m : n, s);
     }
 }
 
@@ -443,7 +532,48 @@ __global__ void __launch_bounds__(256, 1) k_fp8_matmul_big(BigArgs g) {
 
 }  // namespace
 
-size_t fp8_matmul_ws(int64_t M, int64_t N, int64_t k) { return 0; }
+// Which kernel a product takes, and in how many parts of k: the one that an estimate of the time makes fastest.  Half
+// a tile of k takes a workgroup of 64 x 64 entries 0.17 us and the chip 0.155 us for every 256 of them (to fp32 0.31
+// and 0.2), one of 128 x 128 0.32 and 0.32 (0.6 and 0.53), one of 256 x 256, alone on its CU, 0.58 (1.08); the smaller
+// ones' results cost 1 us for 2.5 million, results in parts a second launch and their bytes twice.  Measured, us, 64 / 128 / 256 entries a side: 768 x 768 x 768
+// 6.0 / 8.8 / 13.1; 1024 x 1600 x 1600 10.8 / 13.0 / 17.6; 1024 x 4096 x 4096 42 / 27 / 42; 4800 x 1600 x 4096 79 / 42
+// / 50; 4096 x 4096 x 256 23.5 / 18.4 / 12.5.  In parts: 128 x 4096 x 4096 15.0 in one, 12.8 in two; 300 x 300 x 11008
+// 25 in one, 12.5 in eight; 1600 x 1600 x 16384 83 in one, 60 in two.  Up to 32 rows on one side: 1 x 11008 x 4096
+// 10.3 thin (four waves), 13.7 tiled; 33 rows: 16.1 thin, 14.4 tiled.
+struct MatmulPlan {
+    enum Kind { kThin, kTile64, kTile128, kLarge } kind;
+    int nsplit;                       // parts of k; waves of a thin workgroup
+};
+static MatmulPlan matmul_plan(int64_t M, int64_t N, int64_t k, bool exact) {
+    const int64_t T = fp8_tiles(k);
+    if (std::min(M, N) <= 32) return {MatmulPlan::kThin, T >= 4 ? 4 : T >= 2 ? 2 : 1};
+    auto tiles = [&](int64_t tm) { return ((M + tm - 1) / tm) * ((N + tm - 1) / tm); };
+    const double H = 2.0 * (double)T, big = std::ceil((double)tiles(kBig) / 256);
+    MatmulPlan best{MatmulPlan::kLarge, 1};
+    double cost = 6 + big * (exact ? 4 + 1.08 * H : 3 + 0.58 * H);
+    for (const MatmulPlan::Kind kind : {MatmulPlan::kTile64, MatmulPlan::kTile128}) {
+        const bool small = kind == MatmulPlan::kTile64;
+        const double wgs = (double)tiles(small ? 64 : 128) / 256;
+        const double one = small ? (exact ? 0.31 : 0.17) : exact ? 0.6 : 0.32, all = small ? (exact ? 0.2 : 0.155) : exact ? 0.53 : 0.32;
+        for (int64_t ns = 1; ns <= 32 && ns <= T; ++ns) {
+            const int64_t per = (T + ns - 1) / ns;
+            if ((T + per - 1) / per != ns) continue;
+            const double c = 4 + (double)M * (double)N / 2.5e6 + 2.0 * (double)per * std::max(one, all * wgs * (double)ns) +
+                             (ns > 1 ? 3 + (double)ns * (double)M * (double)N / 0.75e6 : 0.0);
+            if (c < cost) { best = {kind, (int)ns}; cost = c; }
+        }
+    }
+    return best;
+}
+
+size_t fp8_matmul_ws(int64_t M, int64_t N, int64_t k) {
+    size_t need = 0;                  // for a result of either type
+    for (const bool exact : {false, true}) {
+        const MatmulPlan p = matmul_plan(M, N, k, exact);
+        if (p.kind != MatmulPlan::kThin && p.nsplit > 1) need = std::max(need, (size_t)p.nsplit * (size_t)M * (size_t)N * 4);
+    }
+    return need;
+}
 
 hipError_t launch_fp8_matmul(const dobb_fp8_operand &A, const dobb_fp8_operand &B, const void *bias, bool bias_bf16, bool accumulate,
                              void *out, bool out_bf16, int64_t ldo, float *ws, hipStream_t s) {
@@ -452,46 +582,56 @@ hipError_t launch_fp8_matmul(const dobb_fp8_operand &A, const dobb_fp8_operand &
     };
     const Fp8Side a = side(A), b = side(B);
     const Epilogue e{out, bias, ldo, out_bf16, bias_bf16, accumulate};
-    const int64_t halves = 2 * fp8_tiles(A.k);
-#define DOBB_FP8_MM_(TM, TN, FA, FB, EX)                                                                                \
-    do {                                                                                                               \
-        const int64_t tm = (A.rows + TM - 1) / TM, tn = (B.rows + TN - 1) / TN;                                        \
-        if (tm > 0x7fffffff / tn) return hipErrorInvalidValue;                                                         \
-        DOBB_LAUNCH("fp8_matmul", s, (k_fp8_matmul<TM, TN, FA, FB, EX>), dim3((unsigned)(tm * tn)), dim3(256), 0, a, b, halves, (int)tn, e); \
-    } while (0)
-#define DOBB_FP8_MM(TM, TN, FA, FB)                                                                                    \
-    do {                                                                                                               \
-        if (out_bf16) DOBB_FP8_MM_(TM, TN, FA, FB, false);                                                             \
-        else DOBB_FP8_MM_(TM, TN, FA, FB, true);                                                                       \
-    } while (0)
-#define DOBB_FP8_MM_F(TM, TN)                                                                 \
+    const int64_t T = fp8_tiles(A.k);
+    const MatmulPlan p = matmul_plan(A.rows, B.rows, A.k, !out_bf16);
+    auto tiles = [](int64_t rows, int64_t tm) { return (rows + tm - 1) / tm; };
+// L(format of A, of B, exact) for the call's
+#define DOBB_FP8_BY(L)                                                                        \
     do {                                                                                      \
-        if (A.format == DOBB_E4M3 && B.format == DOBB_E4M3) DOBB_FP8_MM(TM, TN, 0, 0);        \
-        else if (A.format == DOBB_E4M3) DOBB_FP8_MM(TM, TN, 0, 1);                            \
-        else if (B.format == DOBB_E4M3) DOBB_FP8_MM(TM, TN, 1, 0);                            \
-        else DOBB_FP8_MM(TM, TN, 1, 1);                                                       \
+        const int f = 2 * (A.format == DOBB_E5M2) + (B.format == DOBB_E5M2);                  \
+        if (out_bf16) {                                                                       \
+            if (f == 0) L(0, 0, false); else if (f == 1) L(0, 1, false); else if (f == 2) L(1, 0, false); else L(1, 1, false); \
+        } else {                                                                              \
+            if (f == 0) L(0, 0, true); else if (f == 1) L(0, 1, true); else if (f == 2) L(1, 0, true); else L(1, 1, true);     \
+        }                                                                                     \
     } while (0)
-    const int64_t tm = (A.rows + kBig - 1) / kBig, tn = (B.rows + kBig - 1) / kBig;
-    if (tm * tn >= 64 && tm * tn < 0x7fffffff - 256 && halves <= 0x7ffffff0) {
-        const BigArgs g{a, b, (uint32_t)tm, (uint32_t)tn, (int)halves, e};
+    if (p.kind == MatmulPlan::kThin) {
+        const bool turned = A.rows > B.rows;
+        const Fp8Side &few = turned ? b : a, &many = turned ? a : b;
+        const dim3 grid((unsigned)tiles(many.rows, 32)), block(64u * p.nsplit);
+#define DOBB_FP8_THIN(F, G, EX)                                                                                                              \
+    do {                                                                                                                                    \
+        if (!turned) DOBB_LAUNCH("fp8_matmul_thin", s, (k_fp8_matmul_thin<F, G, EX>), grid, block, 4096u * p.nsplit, few, many, T, turned, e); \
+        else DOBB_LAUNCH("fp8_matmul_thin", s, (k_fp8_matmul_thin<G, F, EX>), grid, block, 4096u * p.nsplit, few, many, T, turned, e);         \
+    } while (0)
+        DOBB_FP8_BY(DOBB_FP8_THIN);
+#undef DOBB_FP8_THIN
+        return hipGetLastError();
+    }
+    if (p.kind == MatmulPlan::kLarge) {
+        const int64_t tm = tiles(A.rows, kBig), tn = tiles(B.rows, kBig);
+        if (tm * tn >= 0x7fffffff - 256 || 2 * T > 0x7ffffff0) return hipErrorInvalidValue;
+        const BigArgs g{a, b, (uint32_t)tm, (uint32_t)tn, (int)(2 * T), e};
         const dim3 grid((unsigned)std::min<int64_t>(tm * tn, 256));
-#define DOBB_FP8_BIG(FA, FB)                                                                                            \
-    do {                                                                                                               \
-        if (out_bf16) DOBB_LAUNCH("fp8_matmul", s, (k_fp8_matmul_big<FA, FB, false>), grid, dim3(256), 0, g);          \
-        else DOBB_LAUNCH("fp8_matmul", s, (k_fp8_matmul_big<FA, FB, true>), grid, dim3(256), 0, g);                    \
-    } while (0)
-        if (A.format == DOBB_E4M3 && B.format == DOBB_E4M3) DOBB_FP8_BIG(0, 0);
-        else if (A.format == DOBB_E4M3) DOBB_FP8_BIG(0, 1);
-        else if (B.format == DOBB_E4M3) DOBB_FP8_BIG(1, 0);
-        else DOBB_FP8_BIG(1, 1);
+#define DOBB_FP8_BIG(F, G, EX) DOBB_LAUNCH("fp8_matmul", s, (k_fp8_matmul_big<F, G, EX>), grid, dim3(256), 0, g)
+        DOBB_FP8_BY(DOBB_FP8_BIG);
 #undef DOBB_FP8_BIG
         return hipGetLastError();
     }
-    if (A.rows <= 128) DOBB_FP8_MM_F(128, 128);
-    else DOBB_FP8_MM_F(256, 128);
-#undef DOBB_FP8_MM_F
-#undef DOBB_FP8_MM
-#undef DOBB_FP8_MM_
+    const int64_t size = p.kind == MatmulPlan::kTile64 ? 64 : 128, tn = tiles(B.rows, size), wgs = tiles(A.rows, size) * tn * p.nsplit;
+    if (wgs > 0x7fffffff) return hipErrorInvalidValue;
+#define DOBB_FP8_TILE(F, G, EX)                                                                                                        \
+    do {                                                                                                                              \
+        if (size == 64) DOBB_LAUNCH("fp8_matmul", s, (k_fp8_matmul<64, 64, 6, F, G, EX>), dim3((unsigned)wgs), dim3(256), 0, a, b, T, (int)tn, p.nsplit, e, ws); \
+        else DOBB_LAUNCH("fp8_matmul", s, (k_fp8_matmul<128, 128, 4, F, G, EX>), dim3((unsigned)wgs), dim3(256), 0, a, b, T, (int)tn, p.nsplit, e, ws);          \
+    } while (0)
+    DOBB_FP8_BY(DOBB_FP8_TILE);
+#undef DOBB_FP8_TILE
+#undef DOBB_FP8_BY
+    const hipError_t r = hipGetLastError();
+    if (r != hipSuccess || p.nsplit == 1) return r;
+    const int64_t quads = A.rows * ((B.rows + 3) / 4);
+    DOBB_LAUNCH("fp8_join", s, k_fp8_join, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, A.rows, B.rows, p.nsplit, ws, e);
     return hipGetLastError();
 }
 
