@@ -71,12 +71,8 @@ __global__ void __launch_bounds__(256) k_fp8_quantize(int64_t N, int64_t n, int6
     for (int i = 0; i < 8; ++i) unpack8<BF16>(raw[i], v[i]);
     if constexpr (NORM) {
         float w[8], b[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int64_t c = c0 + j < n ? c0 + j : n - 1;
-            w[j] = norm.w ? load1(norm.w, c, norm.w_bf16) : 1.f;
-            b[j] = norm.b ? load1(norm.b, c, norm.w_bf16) : 0.f;
-        }
+        affine8(norm.w, c0, n, norm.w_bf16, 1.f, w);
+        affine8(norm.b, c0, n, norm.w_bf16, 0.f, b);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int64_t r = r0 + i < N ? r0 + i : N - 1;

@@ -14,78 +14,79 @@
 namespace dobb {
 namespace {
 
-// sum over the TPR threads of a row; `sm` holds a float a wave, twice by turns of `turn`
-template <int TPR>
-__device__ __forceinline__ float row_sum(float x, float *sm, int &turn) {
-    x = wave_sum(x);
+// Sums over the TPR threads of a row, of K values at once.  `sm` holds them wave by wave, twice by turns of `turn`; where
+// a row has several waves, every thread of the workgroup takes part.
+template <int TPR, int K>
+__device__ __forceinline__ void row_sums(float (&x)[K], float *sm, int &turn) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) x[k] = TPR == 16 ? sum16(x[k]) : wave_sum(x[k]);
     if constexpr (TPR > 64) {
         constexpr int W = TPR / 64;
-        float *s = sm + W * (turn ^= 1);
-        if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = x;
-        __syncthreads();
-        x = s[0];
+        float *s = sm + (turn ^= 1) * 32 * K;
+        const int wave = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0)
 #pragma unroll
-        for (int k = 1; k < W; ++k) x += s[k];
+            for (int k = 0; k < K; ++k) s[wave * K + k] = x[k];
+        __syncthreads();
+        s += wave / W * W * K;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            x[k] = s[k];
+#pragma unroll
+            for (int w = 1; w < W; ++w) x[k] += s[w * K + k];
+        }
     }
-    return x;
 }
 
-// Rows a workgroup takes at a time, and how they go round: row group g of `groups` takes rows g, g + groups, ..
-template <int TPR>
-constexpr int kThreads = TPR == 64 ? 256 : TPR;
-template <int TPR>
-constexpr int kRowsAt = kThreads<TPR> / TPR;
-
-template <bool XB, int TPR, int CH>
-__global__ void __launch_bounds__(kThreads<TPR>) k_norm(int64_t N, int64_t n, const void *X, int64_t ldx, const void *w, const void *b,
-                                                        bool w_bf16, float eps, void *Y, bool y_bf16, int64_t ldy, float *mean_out,
-                                                        float *rstd_out) {
-    __shared__ float sm[2 * (TPR / 64)];
-    constexpr int RW = kRowsAt<TPR>;
-    const int at = threadIdx.x % TPR;
+// TH threads a workgroup, TPR a row: TH / TPR rows at a time, and workgroup g of `gridDim` takes every gridDim-th such lot
+template <bool XB, int TPR, int CH, int TH>
+__global__ void __launch_bounds__(TH) k_norm(int64_t N, int64_t n, const void *X, int64_t ldx, const void *w, const void *b,
+                                             bool w_bf16, float eps, void *Y, bool y_bf16, int64_t ldy, float *mean_out, float *rstd_out) {
+    __shared__ float sm[128];
+    constexpr int RW = TH / TPR;
+    const int at = threadIdx.x % TPR, sub = TPR < 64 ? threadIdx.x / TPR : __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
     const int64_t stride = (int64_t)gridDim.x * RW;
-    int64_t r = (int64_t)blockIdx.x * RW + threadIdx.x / TPR;
     int turn = 0;
     float wv[CH][8], bv[CH][8];
     if (Y)
 #pragma unroll
-        for (int k = 0; k < CH; ++k)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int64_t c = min<int64_t>((k * TPR + at) * 8 + j, n - 1);
-                wv[k][j] = w ? load1(w, c, w_bf16) : 1.f;
-                bv[k][j] = b ? load1(b, c, w_bf16) : 0.f;
-            }
+        for (int k = 0; k < CH; ++k) {
+            affine8(w, (k * TPR + at) * 8, n, w_bf16, 1.f, wv[k]);
+            affine8(b, (k * TPR + at) * 8, n, w_bf16, 0.f, bv[k]);
+        }
     Raw8<XB> raw[CH];
-    auto fetch = [&](int64_t row) {
+    auto fetch = [&](int64_t row) {              // (rows past the last: that one)
 #pragma unroll
-        for (int k = 0; k < CH; ++k) raw[k] = load8<XB>((const char *)X + row * ldx * (XB ? 2 : 4), (k * TPR + at) * 8, n);
+        for (int k = 0; k < CH; ++k) raw[k] = load8<XB>((const char *)X + min(row, N - 1) * ldx * (XB ? 2 : 4), (k * TPR + at) * 8, n);
     };
     const float inv = 1.f / (float)n;
-    if (r < N) fetch(r);
-    for (; r < N; r += stride) {
+    fetch((int64_t)blockIdx.x * RW + sub);
+    for (int64_t r0 = (int64_t)blockIdx.x * RW; r0 < N; r0 += stride) {
+        const int64_t r = r0 + sub;
         float x[CH][8];
 #pragma unroll
         for (int k = 0; k < CH; ++k) unpack8<XB>(raw[k], x[k]);
-        if (r + stride < N) fetch(r + stride);
-        float s = 0.f;
+        if (r0 + stride < N) fetch(r + stride);
+        float s[1] = {0.f};
 #pragma unroll
         for (int k = 0; k < CH; ++k)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s += x[k][j];
-        const float m0 = row_sum<TPR>(s, sm, turn) * inv;
-        float d = 0.f, q = 0.f;                  // entries past n are zero: left out
+            for (int j = 0; j < 8; ++j) s[0] += x[k][j];
+        row_sums<TPR>(s, sm, turn);
+        const float m0 = s[0] * inv;
+        float dq[2] = {0.f, 0.f};                // entries past n are left out
 #pragma unroll
         for (int k = 0; k < CH; ++k)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float u = (k * TPR + at) * 8 + j < n ? x[k][j] - m0 : 0.f;
-                d += u;
-                q = fmaf(u, u, q);
+                dq[0] += u;
+                dq[1] = fmaf(u, u, dq[1]);
             }
-        d = row_sum<TPR>(d, sm, turn) * inv;
-        q = row_sum<TPR>(q, sm, turn) * inv;
+        row_sums<TPR>(dq, sm + 64, turn);
+        const float d = dq[0] * inv, q = dq[1] * inv;
         const float mean = m0 + d, rstd = 1.f / sqrtf(fmaxf(q - d * d, q * 0.f) + eps);   // (q * 0: NaN stays NaN)
+        if (r >= N) continue;
         if (at == 0) {
             if (mean_out) mean_out[r] = mean;
             if (rstd_out) rstd_out[r] = rstd;
@@ -108,29 +109,30 @@ template <bool XB>
 __global__ void __launch_bounds__(1024) k_norm_long(int64_t N, int64_t n, const void *X, int64_t ldx, const void *w, const void *b,
                                                     bool w_bf16, float eps, void *Y, bool y_bf16, int64_t ldy, float *mean_out,
                                                     float *rstd_out) {
-    __shared__ float sm[32];
+    __shared__ float sm[128];
     int turn = 0;
     const float inv = 1.f / (float)n;
     for (int64_t r = blockIdx.x; r < N; r += gridDim.x) {
         const char *xr = (const char *)X + r * ldx * (XB ? 2 : 4);
-        float s = 0.f, d = 0.f, q = 0.f, x[8];
+        float s[1] = {0.f}, dq[2] = {0.f, 0.f}, x[8];
         for (int64_t c = threadIdx.x * 8; c < n; c += 8192) {
             unpack8<XB>(load8<XB>(xr, c, n), x);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s += x[j];
+            for (int j = 0; j < 8; ++j) s[0] += x[j];
         }
-        const float m0 = row_sum<1024>(s, sm, turn) * inv;
+        row_sums<1024>(s, sm, turn);
+        const float m0 = s[0] * inv;
         for (int64_t c = threadIdx.x * 8; c < n; c += 8192) {
             unpack8<XB>(load8<XB>(xr, c, n), x);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float u = c + j < n ? x[j] - m0 : 0.f;
-                d += u;
-                q = fmaf(u, u, q);
+                dq[0] += u;
+                dq[1] = fmaf(u, u, dq[1]);
             }
         }
-        d = row_sum<1024>(d, sm, turn) * inv;
-        q = row_sum<1024>(q, sm, turn) * inv;
+        row_sums<1024>(dq, sm + 64, turn);
+        const float d = dq[0] * inv, q = dq[1] * inv;
         const float mean = m0 + d, rstd = 1.f / sqrtf(fmaxf(q - d * d, q * 0.f) + eps);
         if (threadIdx.x == 0) {
             if (mean_out) mean_out[r] = mean;
@@ -140,12 +142,11 @@ __global__ void __launch_bounds__(1024) k_norm_long(int64_t N, int64_t n, const 
         char *row = (char *)Y + r * ldy * (y_bf16 ? 2 : 4);
         for (int64_t c = threadIdx.x * 8; c < n; c += 8192) {
             unpack8<XB>(load8<XB>(xr, c, n), x);
-            float y[8];
+            float y[8], wv[8], bv[8];
+            affine8(w, c, n, w_bf16, 1.f, wv);
+            affine8(b, c, n, w_bf16, 0.f, bv);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int64_t e = min<int64_t>(c + j, n - 1);
-                y[j] = norm_value(x[j], mean, rstd, w ? load1(w, e, w_bf16) : 1.f, b ? load1(b, e, w_bf16) : 0.f);
-            }
+            for (int j = 0; j < 8; ++j) y[j] = norm_value(x[j], mean, rstd, wv[j], bv[j]);
             store8(row, c, n, y, y_bf16);
         }
     }
@@ -160,26 +161,27 @@ struct GradPtrs {
     bool w_bf16, dx_bf16;
 };
 
-template <bool DB, bool XB, int TPR, int CH>
-__global__ void __launch_bounds__(kThreads<TPR>) k_norm_grad(int64_t N, int64_t n, GradPtrs p, float *part) {
-    __shared__ float sm[2 * (TPR / 64)];
-    constexpr int RW = kRowsAt<TPR>;
-    const int at = threadIdx.x % TPR;
+template <bool DB, bool XB, int TPR, int CH, int TH>
+__global__ void __launch_bounds__(TH) k_norm_grad(int64_t N, int64_t n, GradPtrs p, float *part) {
+    __shared__ float sm[128];
+    constexpr int RW = TH / TPR;
+    const int at = threadIdx.x % TPR, sub = TPR < 64 ? threadIdx.x / TPR : __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
     const int64_t stride = (int64_t)gridDim.x * RW;
-    int64_t r = (int64_t)blockIdx.x * RW + threadIdx.x / TPR;
     int turn = 0;
     float wv[CH][8], dw[CH][8], db[CH][8];
 #pragma unroll
-    for (int k = 0; k < CH; ++k)
+    for (int k = 0; k < CH; ++k) {
+        affine8(p.w, (k * TPR + at) * 8, n, p.w_bf16, 1.f, wv[k]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            wv[k][j] = p.w ? load1(p.w, min<int64_t>((k * TPR + at) * 8 + j, n - 1), p.w_bf16) : 1.f;
-            dw[k][j] = db[k][j] = 0.f;
-        }
+        for (int j = 0; j < 8; ++j) dw[k][j] = db[k][j] = 0.f;
+    }
     Raw8<XB> rx[CH];
     Raw8<DB> rd[CH];
-    float mean = 0.f, rstd = 0.f;
-    auto fetch = [&](int64_t row) {
+    float mean, rstd;
+    auto fetch = [&](int64_t row) {              // (rows past the last: that one)
+        row = min(row, N - 1);
+        mean = p.mean[row];
+        rstd = p.rstd[row];
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
             rx[k] = load8<XB>((const char *)p.X + row * p.ldx * (XB ? 2 : 4), (k * TPR + at) * 8, n);
@@ -187,37 +189,38 @@ __global__ void __launch_bounds__(kThreads<TPR>) k_norm_grad(int64_t N, int64_t 
         }
     };
     const float inv = 1.f / (float)n;
-    if (r < N) fetch(r);
-    for (; r < N; r += stride) {
-        float h[CH][8], g[CH][8];
-        mean = p.mean[r];
-        rstd = p.rstd[r];
-        float a = 0.f, c = 0.f;
+    fetch((int64_t)blockIdx.x * RW + sub);
+    for (int64_t r0 = (int64_t)blockIdx.x * RW; r0 < N; r0 += stride) {
+        const int64_t r = r0 + sub;
+        const float rs = rstd;
+        float h[CH][8], g[CH][8], ac[2] = {0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
             float x[8], dy[8];
             unpack8<XB>(rx[k], x);
             unpack8<DB>(rd[k], dy);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {        // dy is zero past n
+            for (int j = 0; j < 8; ++j) {        // dy is zero past n, and so are the terms there
                 h[k][j] = (x[j] - mean) * rstd;
-                if ((k * TPR + at) * 8 + j >= n) h[k][j] = 0.f;
-                dw[k][j] = fmaf(dy[j], h[k][j], dw[k][j]);
-                db[k][j] += dy[j];
+                if (r < N) {
+                    dw[k][j] = fmaf(dy[j], h[k][j], dw[k][j]);
+                    db[k][j] += dy[j];
+                }
                 g[k][j] = dy[j] * wv[k][j];
-                a += g[k][j];
-                c = fmaf(g[k][j], h[k][j], c);
+                ac[0] += g[k][j];
+                ac[1] = fmaf(g[k][j], h[k][j], ac[1]);
             }
         }
-        if (r + stride < N) fetch(r + stride);
-        a = row_sum<TPR>(a, sm, turn) * inv;
-        c = row_sum<TPR>(c, sm, turn) * inv;
+        if (r0 + stride < N) fetch(r + stride);
+        row_sums<TPR>(ac, sm, turn);
+        if (r >= N) continue;
+        const float a = ac[0] * inv, c = ac[1] * inv;
         char *row = (char *)p.dX + r * p.lddx * (p.dx_bf16 ? 2 : 4);
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
             float dx[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dx[j] = rstd * (g[k][j] - a - h[k][j] * c);
+            for (int j = 0; j < 8; ++j) dx[j] = rs * (g[k][j] - a - h[k][j] * c);
             store8(row, (k * TPR + at) * 8, n, dx, p.dx_bf16);
         }
     }
@@ -228,25 +231,24 @@ __global__ void __launch_bounds__(kThreads<TPR>) k_norm_grad(int64_t N, int64_t 
         __shared__ float acc[RW - 1][2][8][TPR];
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-            const int wr = threadIdx.x / TPR;
-            if (k > 0) __syncthreads();
-            if (wr > 0)
+            __syncthreads();
+            if (sub > 0)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    acc[wr - 1][0][j][at] = dw[k][j];
-                    acc[wr - 1][1][j][at] = db[k][j];
+                    acc[sub - 1][0][j][at] = dw[k][j];
+                    acc[sub - 1][1][j][at] = db[k][j];
                 }
             __syncthreads();
-            if (wr == 0)
+            if (sub == 0)
+#pragma unroll 1
+                for (int q = 0; q < RW - 1; ++q)
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-#pragma unroll
-                    for (int q = 0; q < RW - 1; ++q) {
+                    for (int j = 0; j < 8; ++j) {
                         dw[k][j] += acc[q][0][j][at];
                         db[k][j] += acc[q][1][j][at];
                     }
         }
-        if (threadIdx.x >= TPR) return;
+        if (sub) return;
     }
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
@@ -258,21 +260,22 @@ __global__ void __launch_bounds__(kThreads<TPR>) k_norm_grad(int64_t N, int64_t 
 // rows that do not fit the registers: dx by rows, read twice ..
 template <bool DB, bool XB>
 __global__ void __launch_bounds__(1024) k_norm_grad_long(int64_t N, int64_t n, GradPtrs p) {
-    __shared__ float sm[32];
+    __shared__ float sm[128];
     int turn = 0;
     const float inv = 1.f / (float)n;
     for (int64_t r = blockIdx.x; r < N; r += gridDim.x) {
         const char *xr = (const char *)p.X + r * p.ldx * (XB ? 2 : 4), *dr = (const char *)p.dY + r * p.lddy * (DB ? 2 : 4);
         const float mean = p.mean[r], rstd = p.rstd[r];
-        float a = 0.f, c = 0.f;
+        float ac[2] = {0.f, 0.f};
         auto eight = [&](int64_t e, float (&g)[8], float (&h)[8]) {
-            float x[8], dy[8];
+            float x[8], dy[8], wv[8];
             unpack8<XB>(load8<XB>(xr, e, n), x);
             unpack8<DB>(load8<DB>(dr, e, n), dy);
+            affine8(p.w, e, n, p.w_bf16, 1.f, wv);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 h[j] = e + j < n ? (x[j] - mean) * rstd : 0.f;
-                g[j] = dy[j] * (p.w ? load1(p.w, min<int64_t>(e + j, n - 1), p.w_bf16) : 1.f);
+                g[j] = dy[j] * wv[j];
             }
         };
         float g[8], h[8];
@@ -280,12 +283,12 @@ __global__ void __launch_bounds__(1024) k_norm_grad_long(int64_t N, int64_t n, G
             eight(e, g, h);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                a += g[j];
-                c = fmaf(g[j], h[j], c);
+                ac[0] += g[j];
+                ac[1] = fmaf(g[j], h[j], ac[1]);
             }
         }
-        a = row_sum<1024>(a, sm, turn) * inv;
-        c = row_sum<1024>(c, sm, turn) * inv;
+        row_sums<1024>(ac, sm, turn);
+        const float a = ac[0] * inv, c = ac[1] * inv;
         char *row = (char *)p.dX + r * p.lddx * (p.dx_bf16 ? 2 : 4);
         for (int64_t e = threadIdx.x * 8; e < n; e += 8192) {
             eight(e, g, h);
@@ -319,36 +322,39 @@ __global__ void __launch_bounds__(256) k_norm_grad_strips(int64_t N, int64_t n, 
     store8(out + n, e, n, db, false);
 }
 
-// the groups' sums in fp64, in order: 32 columns a workgroup, 8 threads a column
-__global__ void __launch_bounds__(256) k_norm_columns(int64_t n, int64_t groups, const float *part, void *dw, void *db, bool g_bf16) {
-    __shared__ double sm[8][32];
+// the groups' sums in fp64, in a fixed order: 32 columns a workgroup, 32 threads a column
+__global__ void __launch_bounds__(1024) k_norm_columns(int64_t n, int64_t groups, const float *part, void *dw, void *db, bool g_bf16) {
+    __shared__ double sm[32][33];
     const int64_t blocks = (n + 31) / 32;
     const bool second = blockIdx.x >= blocks;
-    const int64_t c = (blockIdx.x - (second ? blocks : 0)) * 32 + (threadIdx.x & 31);
-    const int q = threadIdx.x >> 5;
+    const int64_t c0 = (blockIdx.x - (second ? blocks : 0)) * 32;
+    const int col = threadIdx.x & 31, q = threadIdx.x >> 5;
     void *out = second ? db : dw;
     if (!out) return;                            // (the whole workgroup)
-    const float *p = part + (second ? n : 0) + min(c, n - 1);
+    const float *p = part + (second ? n : 0) + min(c0 + col, n - 1);
     double s = 0.0;
     int64_t g = q;
-    for (; g + 24 < groups; g += 32) {
-        float v[4];
+    for (; g + 224 < groups; g += 256) {
+        float v[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = p[(g + 8 * k) * 2 * n];
+        for (int k = 0; k < 8; ++k) v[k] = p[(g + 32 * k) * 2 * n];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) s += (double)v[k];
+        for (int k = 0; k < 8; ++k) s += (double)v[k];
     }
-    for (; g < groups; g += 8) s += (double)p[g * 2 * n];
-    sm[q][threadIdx.x & 31] = s;
+    for (; g < groups; g += 32) s += (double)p[g * 2 * n];
+    sm[q][col] = s;
     __syncthreads();
-    if (q || c >= n) return;
+    // 32 threads a column again, each with one of its sums
+    s = sm[col][q];
 #pragma unroll
-    for (int k = 1; k < 8; ++k) s += sm[k][threadIdx.x];
+    for (int k = 1; k < 32; k *= 2) s += __shfl_xor(s, k);
+    const int64_t c = c0 + q;
+    if (col || c >= n) return;
     if (g_bf16) ((uint16_t *)out)[c] = f32_to_bf16((float)s);
     else ((float *)out)[c] = (float)s;
 }
 
-constexpr int64_t kInRegs = 16384;              // widest rows that stay in registers
+constexpr int64_t kInRegs = 16384;              // widest rows that stay in registers in the forward pass
 
 }  // namespace
 
@@ -360,29 +366,52 @@ hipError_t launch_layer_norm(int64_t N, int64_t n, const void *X, bool x_bf16, i
         else DOBB_LAUNCH("layer_norm", s, k_norm_long<false>, grid, dim3(1024), 0, N, n, X, ldx, w, b, w_bf16, eps, Y, y_bf16, ldy, mean, rstd);
         return hipGetLastError();
     }
-#define DOBB_NORM_(B, TPR, CH)                                                                                         \
-    DOBB_LAUNCH("layer_norm", s, (k_norm<B, TPR, CH>), dim3((unsigned)std::min<int64_t>((N + kRowsAt<TPR> - 1) / kRowsAt<TPR>, 1024)), \
-                dim3(kThreads<TPR>), 0, N, n, X, ldx, w, b, w_bf16, eps, Y, y_bf16, ldy, mean, rstd)
-#define DOBB_NORM(TPR, CH)                   \
-    else if (n <= 8 * (TPR) * (CH)) {        \
-        if (x_bf16) DOBB_NORM_(true, TPR, CH); \
-        else DOBB_NORM_(false, TPR, CH);     \
+#define DOBB_NORM_(B, TPR, CH, TH, WGS)                                                                                 \
+    DOBB_LAUNCH("layer_norm", s, (k_norm<B, TPR, CH, TH>), dim3((unsigned)std::min<int64_t>((N + (TH) / (TPR) - 1) / ((TH) / (TPR)), WGS)), \
+                dim3(TH), 0, N, n, X, ldx, w, b, w_bf16, eps, Y, y_bf16, ldy, mean, rstd)
+#define DOBB_NORM(TPR, CH, TH, WGS)                   \
+    else if (n <= 8 * (TPR) * (CH)) {                 \
+        if (x_bf16) DOBB_NORM_(true, TPR, CH, TH, WGS); \
+        else DOBB_NORM_(false, TPR, CH, TH, WGS);     \
     }
     if (n < 1) return hipErrorInvalidValue;
-    DOBB_NORM(64, 1) DOBB_NORM(64, 2) DOBB_NORM(128, 2) DOBB_NORM(256, 2) DOBB_NORM(512, 2) DOBB_NORM(1024, 2)
+    DOBB_NORM(16, 1, 256, 2048) DOBB_NORM(64, 1, 256, 2048) DOBB_NORM(64, 2, 256, 2048) DOBB_NORM(128, 2, 256, 2048) DOBB_NORM(256, 2, 256, 2048)
+    DOBB_NORM(512, 2, 512, 1024) DOBB_NORM(1024, 2, 1024, 512)
 #undef DOBB_NORM
 #undef DOBB_NORM_
     return hipGetLastError();
 }
 
-// Row groups of the column sums: 512 workgroups, and never more than 1024 rows for one (fp32 sums)
+// How a width is taken: threads a row, chunks of 8 entries a thread, threads a workgroup, and the workgroups that are
+// resident on the chip together (two a CU, one where a thread holds two chunks), each of which leaves its sums.
+// Measured, us: 16384 x 1600 in bf16 with 256 threads a row and 512 workgroups 44, 256 workgroups 66, with 128 threads a
+// row 53; 4096 x 4096 with 512 workgroups of two chunks 27, with 256 23; 16384 x 768 with 64 threads and two chunks 27,
+// with 128 and one 22.
+struct GradShape {
+    int tpr, ch, th;
+    int64_t groups;
+};
+static GradShape grad_shape(int64_t n) {
+    if (n <= 128) return {16, 1, 512, 512};
+    if (n <= 512) return {64, 1, 512, 512};
+    if (n <= 1024) return {128, 1, 512, 512};
+    if (n <= 2048) return {256, 1, 512, 512};
+    if (n <= 4096) return {256, 2, 512, 256};
+    if (n <= 8192) return {512, 2, 512, 256};
+    return {1024, 0, 1024, 64};                  // in two passes
+}
+
+// Row groups of the column sums: with two lots of rows each where there are as many, and never more than 1024 rows
+// (fp32 sums)
 int64_t norm_grad_groups(int64_t N, int64_t n) {
-    const int64_t at = n <= 1024 ? 4 : 1;
-    return std::max<int64_t>(std::min<int64_t>((N + at - 1) / at, 512), (N + 1023) / 1024);
+    const GradShape g = grad_shape(n);
+    const int64_t at = g.th / g.tpr;
+    return std::max<int64_t>(std::min<int64_t>((N + 2 * at - 1) / (2 * at), g.groups), (N + 1023) / 1024);
 }
 
 hipError_t launch_layer_norm_backward(const NormGradArgs &a, hipStream_t s) {
     const int64_t groups = norm_grad_groups(a.N, a.n), n = a.n;
+    const GradShape shape = grad_shape(n);
     const GradPtrs p{a.dY, a.X, a.w, a.mean, a.rstd, a.dX, a.lddy, a.ldx, a.lddx, a.w_bf16, a.dx_bf16};
     float *part = a.dw || a.db ? a.part : nullptr;
     if (n < 1 || groups > 0x7fffffff) return hipErrorInvalidValue;
@@ -393,13 +422,13 @@ hipError_t launch_layer_norm_backward(const NormGradArgs &a, hipStream_t s) {
         else if (a.x_bf16) { L(false, true); }            \
         else { L(false, false); }                         \
     } while (0)
-#define DOBB_GRAD(TPR, CH)                                                                                                             \
-    else if (n <= 8 * (TPR) * (CH)) {                                                                                                  \
-        constexpr int T = TPR, C = CH;                                                                                                 \
-        DOBB_GRAD_T(DOBB_GRAD_L);                                                                                                      \
+#define DOBB_GRAD(TPR, CH, TH)                                        \
+    else if (shape.tpr == (TPR) && shape.ch == (CH)) {                \
+        constexpr int T = TPR, C = CH, H = TH;                        \
+        DOBB_GRAD_T(DOBB_GRAD_L);                                     \
     }
-#define DOBB_GRAD_L(D, B) DOBB_LAUNCH("layer_norm_grad", s, (k_norm_grad<D, B, T, C>), dim3((unsigned)groups), dim3(kThreads<T>), 0, a.N, n, p, part)
-    if (n > kInRegs) {
+#define DOBB_GRAD_L(D, B) DOBB_LAUNCH("layer_norm_grad", s, (k_norm_grad<D, B, T, C, H>), dim3((unsigned)groups), dim3(H), 0, a.N, n, p, part)
+    if (shape.ch == 0) {
         const dim3 grid((unsigned)std::min<int64_t>(a.N, 512));
 #define DOBB_GRAD_LONG(D, B) DOBB_LAUNCH("layer_norm_grad", s, (k_norm_grad_long<D, B>), grid, dim3(1024), 0, a.N, n, p)
         DOBB_GRAD_T(DOBB_GRAD_LONG);
@@ -409,7 +438,7 @@ hipError_t launch_layer_norm_backward(const NormGradArgs &a, hipStream_t s) {
     DOBB_LAUNCH("layer_norm_grad_strips", s, (k_norm_grad_strips<D, B>), dim3((unsigned)(strips * groups)), dim3(256), 0, a.N, n, groups, p, part)
         if (part) DOBB_GRAD_T(DOBB_GRAD_STRIPS);
     }
-    DOBB_GRAD(64, 1) DOBB_GRAD(64, 2) DOBB_GRAD(128, 2) DOBB_GRAD(256, 2) DOBB_GRAD(512, 2) DOBB_GRAD(1024, 2)
+    DOBB_GRAD(16, 1, 512) DOBB_GRAD(64, 1, 512) DOBB_GRAD(128, 1, 512) DOBB_GRAD(256, 1, 512) DOBB_GRAD(256, 2, 512) DOBB_GRAD(512, 2, 512)
 #undef DOBB_GRAD
 #undef DOBB_GRAD_L
 #undef DOBB_GRAD_LONG
@@ -418,7 +447,7 @@ hipError_t launch_layer_norm_backward(const NormGradArgs &a, hipStream_t s) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !part) return e;
     const int64_t blocks = (n + 31) / 32;
-    DOBB_LAUNCH("layer_norm_columns", s, k_norm_columns, dim3((unsigned)(2 * blocks)), dim3(256), 0, n, groups, part, a.dw, a.db, a.g_bf16);
+    DOBB_LAUNCH("layer_norm_columns", s, k_norm_columns, dim3((unsigned)(2 * blocks)), dim3(1024), 0, n, groups, part, a.dw, a.db, a.g_bf16);
     return hipGetLastError();
 }
 

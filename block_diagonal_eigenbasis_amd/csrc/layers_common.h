@@ -76,6 +76,15 @@ __device__ __forceinline__ void store8(void *row, int64_t c, int64_t n, const fl
     }
 }
 
+// entries c .. c + 7 of a weight or bias (zeros from n on), `missing` where there is none
+__device__ __forceinline__ void affine8(const void *p, int64_t c, int64_t n, bool bf16, float missing, float (&v)[8]) {
+    if (!p) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = missing;
+    } else if (bf16) unpack8<true>(load8<true>(p, c, n), v);
+    else unpack8<false>(load8<false>(p, c, n), v);
+}
+
 // What each of a group of 16 lanes receives from a lane of it: exchanges with the lane whose number differs
 // in bit 0, in bit 1, then the mirrored one of 8 and of 16: after the four, a butterfly over 16 lanes.
 template <int STEP>
@@ -89,11 +98,14 @@ __device__ __forceinline__ uint32_t max16(uint32_t x) {
     x = max(x, lane16<2>(x));
     return max(x, lane16<3>(x));
 }
-__device__ __forceinline__ float wave_sum(float x) {
+__device__ __forceinline__ float sum16(float x) {
     x += __uint_as_float(lane16<0>(__float_as_uint(x)));
     x += __uint_as_float(lane16<1>(__float_as_uint(x)));
     x += __uint_as_float(lane16<2>(__float_as_uint(x)));
-    x += __uint_as_float(lane16<3>(__float_as_uint(x)));
+    return x + __uint_as_float(lane16<3>(__float_as_uint(x)));
+}
+__device__ __forceinline__ float wave_sum(float x) {
+    x = sum16(x);
     x += __shfl_xor(x, 16);
     return x + __shfl_xor(x, 32);
 }

@@ -85,5 +85,6 @@ def norm_grad(dy, x, mean, rstd, w):
     ag, agh = np.abs(g).mean(1, keepdims=True), np.abs(g * h).mean(1, keepdims=True)
     dx = rstd[:, None] * (g - a - h * c)
     bound = rstd[:, None] * U * (4 * np.abs(g) + (D + 5) * ag + (D + 9) * np.abs(h) * agh)
-    rows = -(-x.shape[0] // 512) + 6
+    # a column's sum: a thread's rows (of at least 64 groups), then up to 32 threads of a group; the groups in fp64
+    rows = -(-x.shape[0] // 64) + 32
     return (dx, (dy * h).sum(0), dy.sum(0)), (bound, (rows + 3) * U * np.abs(dy * h).sum(0), rows * U * np.abs(dy).sum(0))
