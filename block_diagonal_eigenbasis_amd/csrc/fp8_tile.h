@@ -70,7 +70,8 @@ __device__ __forceinline__ bf16x8 fp8_to_bf16(int lo, int hi, float scale) {
 }
 
 // FA, FB: formats of the operands; acc[i][j]: rows 32 i .. of the wave's A side, 32 j .. of its B side
-template <int TM, int TN, int NS, int FA, int FB, bool EXACT>
+// SQUARE: both sides are one operand (TM = TN), of which each wave multiplies the pairs of `pairs` (bit kFN i + j)
+template <int TM, int TN, int NS, int FA, int FB, bool EXACT, bool SQUARE = false>
 struct Fp8Tile {
     static constexpr int kWM = TM / 2, kWN = TN / 2;             // of a wave
     static constexpr int kFM = kWM / 32, kFN = kWN / 32;
@@ -81,13 +82,16 @@ struct Fp8Tile {
     uint32_t offA[TM / 64], offB[TN / 64], offS;
     Fp8Side a, b;
     bool scale_of_b;
-    int wave;
+    int wave, part;                   // part: the quarter that this wave multiplies
+    uint32_t pairs = ~0u;
+    bool same = false;                // the sides are the same rows: B's are not loaded again
 
     // Rows are read from a multiple of four (scales come by fours): a side's row0 may be any where the tile
     // leaves room, `fr` then being the place of a wave's rows in the slot.
     __device__ __forceinline__ Fp8Tile(const Fp8Side &a_, const Fp8Side &b_) : a(a_), b(b_) {
         const int lane = threadIdx.x & 63;
-        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        part = wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        same = SQUARE && a.row0 == b.row0;
 #pragma unroll
         for (int k = 0; k < TM / 64; ++k) {
             const uint32_t r = a.row0 + 64 * k + lane;
@@ -96,7 +100,7 @@ struct Fp8Tile {
 #pragma unroll
         for (int k = 0; k < TN / 64; ++k) {
             const uint32_t r = b.row0 + 64 * k + lane;
-            offB[k] = r < b.end ? ((uint32_t)wave * b.rows + r) * 16 : kFp8Off;
+            offB[k] = r < b.end && !same ? ((uint32_t)wave * b.rows + r) * 16 : kFp8Off;
         }
         // scales: 64 words from the word that holds row0's, by waves 0 and 2 of A, 1 and 3 of B
         scale_of_b = wave & 1;
@@ -121,24 +125,33 @@ struct Fp8Tile {
 #pragma unroll
         for (int k = 0; k < TN / 64; ++k) lds_load16(rb, buf + kB + (wave * TN + 64 * k) * 16, offB[k]);
     }
-    __device__ __forceinline__ void multiply(const uint8_t *buf, f32x16 (&acc)[kFM][kFN]) const {
-        const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
-        const int ra = (wave >> 1) * kWM + col, rb = (wave & 1) * kWN + col;
-        const uint8_t *sa = buf + kPieces + (a.row0 & 3u), *sb = buf + kPieces + 256 + (b.row0 & 3u);
+    struct Frags {                               // a wave's operands of half a tile, and their scales
         i32x8 x[kFM], y[kFN];
         uint32_t ea[kFM], eb[kFN];
+    };
+    __device__ __forceinline__ void read(const uint8_t *buf, Frags &f) const {
+        const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
+        const int ra = (part >> 1) * kWM + col, rb = (part & 1) * kWN + col;
+        const uint8_t *sa = buf + kPieces + (a.row0 & 3u), *sb = buf + kPieces + 256 + (b.row0 & 3u);
+        const uint8_t *bb = buf + (SQUARE && same ? 0 : kB);
 #pragma unroll
         for (int i = 0; i < kFM; ++i) {
             const i32x4 lo = *(const i32x4 *)(buf + (half * TM + ra + 32 * i) * 16), hi = *(const i32x4 *)(buf + ((half + 2) * TM + ra + 32 * i) * 16);
-            x[i] = i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            ea[i] = sa[ra + 32 * i];
+            f.x[i] = i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            f.ea[i] = sa[ra + 32 * i];
         }
 #pragma unroll
         for (int j = 0; j < kFN; ++j) {
-            const i32x4 lo = *(const i32x4 *)(buf + kB + (half * TN + rb + 32 * j) * 16), hi = *(const i32x4 *)(buf + kB + ((half + 2) * TN + rb + 32 * j) * 16);
-            y[j] = i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            eb[j] = sb[rb + 32 * j];
+            const i32x4 lo = *(const i32x4 *)(bb + (half * TN + rb + 32 * j) * 16), hi = *(const i32x4 *)(bb + ((half + 2) * TN + rb + 32 * j) * 16);
+            f.y[j] = i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            f.eb[j] = sb[rb + 32 * j];
         }
+    }
+    __device__ __forceinline__ void multiply(const Frags &f, f32x16 (&acc)[kFM][kFN]) const {
+        const auto &x = f.x;
+        const auto &y = f.y;
+        const auto &ea = f.ea;
+        const auto &eb = f.eb;
         // B's rows are the accumulator's rows: a lane then holds four neighbouring columns of the output at a time
         if constexpr (EXACT) {
             float fa[kFM], fb[kFN];
@@ -146,6 +159,25 @@ struct Fp8Tile {
             for (int i = 0; i < kFM; ++i) fa[i] = __uint_as_float(ea[i] << 23);
 #pragma unroll
             for (int j = 0; j < kFN; ++j) fb[j] = __uint_as_float(eb[j] << 23);
+            if constexpr (SQUARE) {
+                if (!pairs) return;
+                bf16x8 p[kFM][4], q[kFN][4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                    for (int i = 0; i < kFM; ++i) p[i][k] = fp8_to_bf16<FA>(x[i][2 * k], x[i][2 * k + 1], fa[i]);
+#pragma unroll
+                    for (int j = 0; j < kFN; ++j) q[j][k] = fp8_to_bf16<FB>(y[j][2 * k], y[j][2 * k + 1], fb[j]);
+                }
+#pragma unroll
+                for (int i = 0; i < kFM; ++i)
+#pragma unroll
+                    for (int j = 0; j < kFN; ++j)
+                        if (pairs >> (kFN * i + j) & 1)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q[j][k], p[i][k], acc[i][j], 0, 0, 0);
+                return;
+            }
 #pragma unroll
             for (int k = 0; k < 8; k += 2) {
                 bf16x8 p[kFM], q[kFN];
@@ -167,6 +199,8 @@ struct Fp8Tile {
                 acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(y[j], x[i], acc[i][j], FB, FA, 0, (int)eb[j], 0, (int)ea[i]);
     }
     // acc += the products over half tiles h0 .. h1 - 1.  On return no load is in flight and every wave is done with LDS.
+    // (Reading the next half's operands while this one's are multiplied measured no faster: two or three workgroups on
+    // each CU cover the reads, and the registers cost one of three.)
     __device__ __forceinline__ void run(int64_t h0, int64_t h1, uint8_t *const (&buf)[NS], f32x16 (&acc)[kFM][kFN]) const {
 #pragma unroll
         for (int k = 0; k < NS - 1; ++k) issue(h0 + k, h1, buf[k]);
@@ -177,7 +211,9 @@ struct Fp8Tile {
             for (int k = 0; k < 2 * NS; ++k) {
                 if (h + k >= h1) break;
                 issue(h + k + NS - 1, h1, buf[(k + NS - 1) % NS]);
-                multiply(buf[k % NS], acc);
+                Frags f;
+                read(buf[k % NS], f);
+                multiply(f, acc);
                 fp8_vm_wait<(NS - 2) * kLoads>();
                 fp8_barrier();
             }

@@ -49,8 +49,7 @@ template <int F, bool NT>
 __global__ void __launch_bounds__(256, 2) k_moment_mx4_narrow(int cnt, int nb, int64_t tiles, int whole, int nsplit_, double beta,
                                                               double scale, float *partial, MomentTable t) {
     constexpr int PAIRS = F * (F + 1) / 2;
-    constexpr int PH = PAIRS > 6 ? 5 : PAIRS;   // pairs that are added up at a time
-    __shared__ f32x4 sm[PH][3][4][64];          // accumulators on their way from wave to wave, lane to lane
+    __shared__ PairSums<F> sm;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 31, half = lane >> 5;
     const Place pl = place(whole, nsplit_, 1);
@@ -127,53 +126,10 @@ __global__ void __launch_bounds__(256, 2) k_moment_mx4_narrow(int cnt, int nb, i
     }
 #undef DOBB_MX4_GROUP
 
-    // Pair p ends up with wave p % 4: the others hand it their sums through LDS, and it adds them in
-    // the order of the waves behind it and stores the pair.
     const int64_t nbb = (int64_t)nb * nb;
     const bool part = pl.nsplit > 1;
     float *out = part ? partial + ((int64_t)(blk - whole) * pl.nsplit + pl.split) * nbb : t.A[mat] + (blk - t.first[mat]) * nbb;
-    constexpr int OWN = (PAIRS + 3) / 4;        // pairs wave, wave + 4, ..
-    int fi[OWN], fj[OWN];
-#pragma unroll
-    for (int o = 0; o < OWN; ++o) {
-        fi[o] = 0;
-        fj[o] = 4 * o + wave;
-        while (fj[o] > fi[o]) fj[o] -= ++fi[o];
-    }
-    const bool old = !part && beta > 0.0;
-    float av[2][16];
-    f32x16 own[OWN];
-#pragma unroll
-    for (int h = 0; h < PAIRS; h += PH) {
-        if (h > 0) __syncthreads();
-#pragma unroll
-        for (int p = h; p < h + PH && p < PAIRS; ++p)
-            if (wave != p % 4)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    sm[p - h][(wave + 3 - p) & 3][k][lane] = f32x4{acc[p][4 * k], acc[p][4 * k + 1], acc[p][4 * k + 2], acc[p][4 * k + 3]};
-        __syncthreads();
-#pragma unroll
-        for (int p = h; p < h + PH && p < PAIRS; ++p)
-            if (wave == p % 4) {
-                f32x4 x[3][4];
-#pragma unroll
-                for (int s = 0; s < 3; ++s)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) x[s][k] = sm[p - h][s][k][lane];
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    own[p / 4][r] = ((acc[p][r] + x[0][r >> 2][r & 3]) + x[1][r >> 2][r & 3]) + x[2][r >> 2][r & 3];
-            }
-    }
-#pragma unroll
-    for (int o = 0; o < OWN; ++o) {             // the old entries of the next pair read before the stores of this one
-        if (old && o == 0) read_pair(out, nb, 32 * fi[0], 32 * fj[0], av[0]);
-        if (old && o + 1 < OWN) read_pair(out, nb, 32 * fi[o + 1], 32 * fj[o + 1], av[(o + 1) & 1]);
-        batch();
-        if (4 * o + wave < PAIRS) store_pair(out, nb, 32 * fi[o], 32 * fj[o], own[o], av[o & 1], part, beta, scale);
-        batch();
-    }
+    finish_pairs<F>(acc, sm, out, nb, part, beta, scale);
 }
 
 // ---- wide ----------------------------------------------------------------------------------------
@@ -422,26 +378,7 @@ MomentPlan moment_mx4_plan(int64_t nb, int64_t blocks, int64_t tiles) {
         }
         return t;
     };
-    const int64_t least = (tp + kSplitPairs - 1) / kSplitPairs;
-    MomentPlan best{0, 1};
-    double cost = 1e300;
-    const int64_t full = blocks * nwg / slots * slots / nwg;
-    for (const int64_t whole : {blocks, full, (int64_t)0}) {
-        if (whole > 0 && least > 1) continue;
-        const int64_t rest = blocks - whole;
-        for (int64_t ns = least; ns <= tp && ns <= least + 63; ++ns) {
-            const int64_t per = (tp + ns - 1) / ns;
-            if ((tp + per - 1) / per != ns) continue;
-            const double c = run(whole * nwg, tp) + (rest ? run(rest * nwg * ns, per) : 0.0) +
-                             (rest && ns > 1 ? 5.0 + partial * (double)(rest * ns) : 0.0);
-            if (c < cost) { best = rest && ns > 1 ? MomentPlan{(int)whole, (int)ns} : MomentPlan{(int)blocks, 1}; cost = c; }
-        }
-    }
-    if (cost == 1e300) {                                   // no even count of splits in the range
-        const int64_t per = (tp + least - 1) / least;
-        best = {0, (int)((tp + per - 1) / per)};
-    }
-    return best;
+    return moment_plan(blocks, nwg, slots, tp, kSplitPairs, partial, run);
 }
 
 hipError_t launch_moment_reduce(const MomentArgs &a, const MomentTable &t, int64_t blocks, hipStream_t s) {
