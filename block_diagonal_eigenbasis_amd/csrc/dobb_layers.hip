@@ -16,7 +16,7 @@ dobb_status check_matrix(const void *p, int64_t N, int64_t n, dobb_dtype dt, int
     if (!p) return DOBB_ERR_INVALID_ARG;
     if (!dtype_ok(dt)) return DOBB_ERR_DTYPE;
     if (N < 1) return DOBB_ERR_INVALID_ARG;
-    if (n < 1 || n > kMaxN || ld < n || ld > ((int64_t)1 << 40)) return DOBB_ERR_SHAPE;
+    if (n < 1 || n > kMaxN || ld < n || N > kMaxTokens || ld > (((int64_t)1 << 60) / N)) return DOBB_ERR_SHAPE;   // bytes in 64 bits
     return aligned(p, (uintptr_t)size_of(dt)) ? DOBB_OK : DOBB_ERR_INVALID_ARG;
 }
 

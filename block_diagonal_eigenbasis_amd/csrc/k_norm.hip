@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(TH) k_norm_grad(int64_t N, int64_t n, GradPtrs
     }
 }
 
-// rows that do not fit the registers: dx by rows, read twice ..
+// rows that do not fit the registers: dx by rows, read twice,
 template <bool DB, bool XB>
 __global__ void __launch_bounds__(1024) k_norm_grad_long(int64_t N, int64_t n, GradPtrs p) {
     __shared__ float sm[128];
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(1024) k_norm_grad_long(int64_t N, int64_t n, G
     }
 }
 
-// .. and the column sums by strips of 2048 columns and groups of rows (group g takes rows g, g + groups, ..)
+// and before that the column sums by strips of 2048 columns and groups of rows (group g takes rows g, g + groups, ..)
 template <bool DB, bool XB>
 __global__ void __launch_bounds__(256) k_norm_grad_strips(int64_t N, int64_t n, int64_t groups, GradPtrs p, float *part) {
     const int64_t strips = (n + 2047) / 2048, g = blockIdx.x / strips;
@@ -428,15 +428,15 @@ hipError_t launch_layer_norm_backward(const NormGradArgs &a, hipStream_t s) {
         DOBB_GRAD_T(DOBB_GRAD_L);                                     \
     }
 #define DOBB_GRAD_L(D, B) DOBB_LAUNCH("layer_norm_grad", s, (k_norm_grad<D, B, T, C, H>), dim3((unsigned)groups), dim3(H), 0, a.N, n, p, part)
-    if (shape.ch == 0) {
+    if (shape.ch == 0) {                         // the sums first: dX may be dY itself
         const dim3 grid((unsigned)std::min<int64_t>(a.N, 512));
-#define DOBB_GRAD_LONG(D, B) DOBB_LAUNCH("layer_norm_grad", s, (k_norm_grad_long<D, B>), grid, dim3(1024), 0, a.N, n, p)
-        DOBB_GRAD_T(DOBB_GRAD_LONG);
         const int64_t strips = (n + 2047) / 2048;
         if (strips > 0x7fffffff / groups) return hipErrorInvalidValue;
 #define DOBB_GRAD_STRIPS(D, B) \
     DOBB_LAUNCH("layer_norm_grad_strips", s, (k_norm_grad_strips<D, B>), dim3((unsigned)(strips * groups)), dim3(256), 0, a.N, n, groups, p, part)
         if (part) DOBB_GRAD_T(DOBB_GRAD_STRIPS);
+#define DOBB_GRAD_LONG(D, B) DOBB_LAUNCH("layer_norm_grad", s, (k_norm_grad_long<D, B>), grid, dim3(1024), 0, a.N, n, p)
+        DOBB_GRAD_T(DOBB_GRAD_LONG);
     }
     DOBB_GRAD(16, 1, 512) DOBB_GRAD(64, 1, 512) DOBB_GRAD(128, 1, 512) DOBB_GRAD(256, 1, 512) DOBB_GRAD(256, 2, 512) DOBB_GRAD(512, 2, 512)
 #undef DOBB_GRAD

@@ -228,6 +228,27 @@ def test_matmul_not_finite_and_wide_scales(M, N):
     assert bool((dobb.dobb_fp8_matmul(z, z, dtype=F32) == 0).all())
 
 
+@pytest.mark.parametrize("M,N", [(2, 40), (200, 300), (2050, 2060)])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_matmul_smallest_scale_and_not_finite_by_format(M, N, fmt):
+    """Rows at the least power of two, 2^-127, against rows near the largest values; NaN of either format."""
+    tiny = values(M, 200, 1).clamp(-4, 4) * 2.0 ** -120
+    tiny[tiny.abs() < 2.0 ** -126 * 2.0 ** 9] = 2.0 ** -118         # (every entry's value in bf16's normal range)
+    huge = values(N, 200, 2).clamp(-4, 4) * 2.0 ** 118
+    a, b = dobb.dobb_fp8_quantize(tiny, fmt=fmt)[0], dobb.dobb_fp8_quantize(huge, fmt=fmt)[0]
+    for dtype in (F32, BF16):
+        check_matmul(a, b, dtype)
+        check_matmul(b, a, dtype)
+    assert int(a.scales.min()) <= 8
+    bad = values(M, 200, 3)
+    bad[M - 1, 150] = float("nan")
+    c, d = dobb.dobb_fp8_quantize(bad, fmt=fmt)[0], dobb.dobb_fp8_quantize(values(N, 200, 4), fmt=fmt)[0]
+    for dtype in (F32, BF16):
+        got, turned = dobb.dobb_fp8_matmul(c, d, dtype=dtype), dobb.dobb_fp8_matmul(d, c, dtype=dtype)
+        assert bool(got[M - 1].isnan().all()) and bool(got[:M - 1].isfinite().all())
+        assert bool(turned[:, M - 1].isnan().all()) and bool(turned[:, :M - 1].isfinite().all())
+
+
 def test_matmul_repeats_bit_for_bit_and_k_of_a_joined_capture():
     a, b = operand(700, 4000, 1), operand(900, 4000, 2)
     for dtype in (F32, BF16):
@@ -305,11 +326,14 @@ def test_moment_grouped_mixed_widths_and_shared_captures():
     assert all(torch.equal(a, b) for a, b in zip(As, again))
 
 
-def test_moment_not_finite_stays_in_its_rows():
-    x = values(200, 96, 1)
-    clean = dobb.dobb_accumulate_moment_fp8(dobb.dobb_fp8_quantize(x, rows=False, cols=True)[1], torch.empty(3, 32, 32, device=DEV), 32)
-    x[150, 40] = float("nan")
-    A = dobb.dobb_accumulate_moment_fp8(dobb.dobb_fp8_quantize(x, rows=False, cols=True)[1], torch.empty(3, 32, 32, device=DEV), 32)
+@pytest.mark.parametrize("nb", [32, 120, 200])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_moment_not_finite_stays_in_its_rows(nb, fmt):
+    x = values(200, 3 * nb, 1)
+    new = lambda: torch.empty(3, nb, nb, device=DEV)  # noqa: E731
+    clean = dobb.dobb_accumulate_moment_fp8(dobb.dobb_fp8_quantize(x, rows=False, cols=True, fmt=fmt)[1], new(), nb)
+    x[150, nb + 8] = float("nan")
+    A = dobb.dobb_accumulate_moment_fp8(dobb.dobb_fp8_quantize(x, rows=False, cols=True, fmt=fmt)[1], new(), nb)
     assert bool(A[1, 8].isnan().all()) and bool(A[1, :, 8].isnan().all())
     A[1, 8], A[1, :, 8] = clean[1, 8], clean[1, :, 8]
     assert torch.equal(A, clean)

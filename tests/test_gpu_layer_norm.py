@@ -172,6 +172,19 @@ def test_backward_targets_and_in_place():
     assert torch.equal(big[:, 5:518], dx) and bool((big[:, :5] == 3.0).all()) and bool((big[:, 518:] == 3.0).all())
 
 
+@pytest.mark.parametrize("n", [100, 600, 1600, 3000, 8000, 8193, 17000])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_backward_in_place_at_every_width(n, dtype):
+    """dX written over dY, rows read once or twice: the sums are those of the gradient as it was."""
+    x, dy, w = rand(131, n, seed=1, dtype=dtype), rand(131, n, seed=2, dtype=dtype), rand(n, seed=3)
+    _, mean, rstd = dobb.dobb_layer_norm(x, w)
+    want = dobb.dobb_layer_norm_backward(dy, x, mean, rstd, w)
+    got = dobb.dobb_layer_norm_backward(dy, x, mean, rstd, w, dX=dy)
+    assert got[0].data_ptr() == dy.data_ptr() and all(torch.equal(p, q) for p, q in zip(got, want))
+    y = dobb.dobb_layer_norm(x, w)[0]
+    assert torch.equal(dobb.dobb_layer_norm(x, w, out=x)[0], y)
+
+
 def test_backward_against_differences():
     """The gradient of sum(c y) for fixed c, by central differences of the forward pass in 64 bits."""
     x, w, b, c = rand(3, 40, seed=1), rand(40, seed=2, shift=1.0), rand(40, seed=3), rand(3, 40, seed=4)

@@ -38,7 +38,7 @@ def test_layer_norm_refusals():
     nan, inf = float("nan"), float("inf")
     assert _norm(x=None) == INVALID and _norm(y=None) == INVALID
     assert _norm(N=0) == INVALID and _norm(n=0) == SHAPE and _norm(N=BIG + 1) == SHAPE and _norm(n=BIG + 1, ldx=BIG + 1, ldy=BIG + 1) == SHAPE
-    assert _norm(ldx=7) == SHAPE and _norm(ldy=7) == SHAPE
+    assert _norm(ldx=7) == SHAPE and _norm(ldy=7) == SHAPE and _norm(ldx=1 << 60) == SHAPE and _norm(N=BIG, ldy=1 << 50) == SHAPE
     assert _norm(xt=2) == DTYPE and _norm(yt=-1) == DTYPE and _norm(wt=9) == DTYPE
     assert _norm(eps=-1e-9) == INVALID and _norm(eps=nan) == INVALID and _norm(eps=inf) == INVALID
     assert _norm(x=X + 2) == INVALID and _norm(y=Y + 1, yt=1) == INVALID and _norm(w=W + 2) == INVALID and _norm(mean=Z + 2) == INVALID
