@@ -252,7 +252,7 @@ dobb_status dobb_fp8_dequantize(const dobb_fp8_operand *op, int32_t transpose, v
         const int64_t R = transpose ? op->k : op->rows, C = transpose ? op->rows : op->k;
         st = check_matrix(out, R, C, out_dtype, ldo);
         if (st != DOBB_OK) return st;
-        if (fp8_tiles(op->k) > 0x7fffffff / fp8_tiles(op->rows)) return DOBB_ERR_SHAPE;
+        if (fp8_tiles(op->k) > 0x1fffffff / fp8_tiles(op->rows)) return DOBB_ERR_SHAPE;   // workgroups of 32 rows of a tile
         Spans s;
         s.operand(*op, false);
         s.matrix(out, R, C, out_dtype, ldo, true);

@@ -207,67 +207,52 @@ __device__ __forceinline__ void values16(const uint4 &q, uint32_t byte, float (&
         for (int k = 0; k < 16; ++k) v[k] = nan;
 }
 
-// rows x k: a workgroup takes 128 rows of a tile, 8 lanes a row, 32 or 64 bytes a lane
+// rows x k: a workgroup takes 32 rows of a tile, 8 lanes a row, 32 or 64 bytes a lane
 template <int FMT>
 __global__ void __launch_bounds__(256) k_fp8_dequantize(int64_t R, int64_t K, unsigned rowblocks, const uint4 *codes,
                                                         const uint8_t *scales, void *out, bool bf16, int64_t ldo) {
     const int64_t t = blockIdx.x / rowblocks, rb = blockIdx.x % rowblocks;
     const int h = threadIdx.x & 7;
-    const int64_t pitch = (R + 3) / 4 * 4, c = t * 128 + 16 * h;
-    uint4 q[4];
-    uint32_t e[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int64_t r = min<int64_t>(rb * 128 + 32 * k + (threadIdx.x >> 3), R - 1);
-        q[k] = codes[(t * 8 + h) * R + r];
-        e[k] = scales[t * pitch + r];
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int64_t r = rb * 128 + 32 * k + (threadIdx.x >> 3);
-        if (r >= R) break;
-        float v[16];
-        values16<FMT>(q[k], e[k], v);
-        char *row = (char *)out + r * ldo * (bf16 ? 2 : 4);
-        const float lo[8] = {v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]}, hi[8] = {v[8], v[9], v[10], v[11], v[12], v[13], v[14], v[15]};
-        store8(row, c, K, lo, bf16);
-        store8(row, c + 8, K, hi, bf16);
-    }
+    const int64_t pitch = (R + 3) / 4 * 4, c = t * 128 + 16 * h, r = rb * 32 + (threadIdx.x >> 3);
+    if (r >= R) return;
+    float v[16];
+    values16<FMT>(codes[(t * 8 + h) * R + r], scales[t * pitch + r], v);
+    char *row = (char *)out + r * ldo * (bf16 ? 2 : 4);
+    const float lo[8] = {v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]}, hi[8] = {v[8], v[9], v[10], v[11], v[12], v[13], v[14], v[15]};
+    store8(row, c, K, lo, bf16);
+    store8(row, c + 8, K, hi, bf16);
 }
 
 struct __attribute__((packed, aligned(2))) PairBf16 { uint32_t w; };
 struct __attribute__((packed, aligned(4))) PairF32 { float a, b; };
 
-// k x rows: a workgroup takes 128 rows of a tile, two neighbouring ones a lane, a wave two of the 16-entry groups
+// k x rows: a workgroup takes 128 rows of half a tile, two neighbouring ones a lane, a wave one of the 16-entry groups
 template <int FMT>
 __global__ void __launch_bounds__(256) k_fp8_dequantize_t(int64_t R, int64_t K, unsigned rowblocks, const uint4 *codes,
                                                           const uint8_t *scales, void *out, bool bf16, int64_t ldo) {
-    const int64_t t = blockIdx.x / rowblocks, rb = blockIdx.x % rowblocks;
+    const int64_t t = blockIdx.x / rowblocks / 2, rb = blockIdx.x % rowblocks;
     const int64_t r = rb * 128 + 2 * (threadIdx.x & 63), pitch = (R + 3) / 4 * 4;
+    const int h = (threadIdx.x >> 6) + 4 * (blockIdx.x / rowblocks & 1);
     if (r >= R) return;
     const bool two = r + 1 < R;
     const uint32_t ea = scales[t * pitch + r], eb = two ? scales[t * pitch + r + 1] : 0;
+    const uint4 *p = codes + (t * 8 + h) * R + r;
+    const uint4 qa = p[0], qb = two ? p[1] : uint4{0, 0, 0, 0};
+    float a[16], b[16];
+    values16<FMT>(qa, ea, a);
+    values16<FMT>(qb, eb, b);
+    const int64_t k0 = t * 128 + 16 * h;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int h = (threadIdx.x >> 6) + 4 * u;
-        const uint4 *p = codes + (t * 8 + h) * R + r;
-        const uint4 qa = p[0], qb = two ? p[1] : uint4{0, 0, 0, 0};
-        float a[16], b[16];
-        values16<FMT>(qa, ea, a);
-        values16<FMT>(qb, eb, b);
-        const int64_t k0 = t * 128 + 16 * h;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            if (k0 + k >= K) break;
-            if (bf16) {
-                uint16_t *x = (uint16_t *)out + (k0 + k) * ldo + r;
-                if (two) ((PairBf16 *)x)->w = pack_bf16(a[k], b[k]);
-                else *x = f32_to_bf16(a[k]);
-            } else {
-                float *x = (float *)out + (k0 + k) * ldo + r;
-                if (two) *(PairF32 *)x = PairF32{a[k], b[k]};
-                else *x = a[k];
-            }
+    for (int k = 0; k < 16; ++k) {
+        if (k0 + k >= K) break;
+        if (bf16) {
+            uint16_t *x = (uint16_t *)out + (k0 + k) * ldo + r;
+            if (two) ((PairBf16 *)x)->w = pack_bf16(a[k], b[k]);
+            else *x = f32_to_bf16(a[k]);
+        } else {
+            float *x = (float *)out + (k0 + k) * ldo + r;
+            if (two) *(PairF32 *)x = PairF32{a[k], b[k]};
+            else *x = a[k];
         }
     }
 }
@@ -304,7 +289,7 @@ hipError_t launch_fp8_quantize(int64_t N, int64_t n, const void *X, bool bf16, i
 }
 
 hipError_t launch_fp8_dequantize(const dobb_fp8_operand &op, bool transpose, void *out, bool bf16, int64_t ldo, hipStream_t s) {
-    const int64_t rb = (op.rows + 127) / 128, T = fp8_tiles(op.k);
+    const int64_t rb = transpose ? (op.rows + 127) / 128 : (op.rows + 31) / 32, T = fp8_tiles(op.k) * (transpose ? 2 : 1);
     if (T > 0x7fffffff / rb) return hipErrorInvalidValue;
     const dim3 grid((unsigned)(T * rb));
 #define DOBB_FP8_READ(K, F)                                                                                            \

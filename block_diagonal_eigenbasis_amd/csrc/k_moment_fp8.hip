@@ -154,22 +154,26 @@ __global__ void __launch_bounds__(256, 2) k_moment_fp8_wide(int cnt, int nb, int
 
 }  // namespace
 
-// How a launch splits its tokens (moment_plan).  A tile takes a narrow workgroup 0.34 us (four at once; 1.8 us at 128
-// columns where all slots read at the memory's rate), a wide one 2 us where three are on each CU.
+// How a launch splits its tokens (moment_plan).  A tile takes a narrow workgroup 0.12 us a fragment (four at once; 1.8 us
+// at 128 columns where all slots read at the memory's rate), a wide one 1.2 us alone on its CU and 2 us beside two others.
+// Wide blocks are split all or none: workgroups of a second round begin as those of the first end, so that no round of
+// whole blocks ends at once (16384 tokens, 192 blocks of 400: none split 707 us, all in two 693, 39 of them in two 771;
+// 16 blocks: 149 whole, 107 in two, 78 in four, 77 in eight, 89 in sixteen; 32 blocks of 128: 63 whole, 28 in four, 27 in
+// eight, 37 in sixteen).
 MomentPlan moment_fp8_plan(int64_t nb, int64_t blocks, int64_t tiles) {
     const bool narrow = nb <= kNarrow;
     const int64_t nwg = narrow ? 1 : tile_pairs(nb), slots = narrow ? (nb <= 96 ? 512 : 256) : 768;
     auto run = [&](int64_t wgs, int64_t units) {
         double t = 0.0;
         for (; wgs > 0; wgs -= std::min(wgs, slots)) {
-            const double full = (double)std::min(wgs, slots) / (double)slots;
-            const double w = (double)slots / 512 * 1.8 * (double)nb / 128;
-            t += narrow ? std::max(0.34 * (double)((units + 3) / 4 * 4), full * w * (double)units) : std::max(0.7, 2.0 * full) * (double)units;
-            if (wgs > 64 * slots) return t * (double)wgs / (double)slots;
+            const double now = (double)std::min(wgs, slots), w = 1.8 / 512 * (double)nb / 128;
+            t += narrow ? std::max(0.12 * (double)((nb + 31) / 32) * (double)((units + 3) / 4 * 4), now * w * (double)units)
+                        : std::max(1.17, 0.75 + 0.42 / 256 * now) * (double)units;
+            if (wgs > 64 * slots) return t * (double)wgs / now;
         }
         return t;
     };
-    return moment_plan(blocks, nwg, slots, tiles, kSplitTiles, (double)nb * (double)nb * 8 / 5e6, run);
+    return moment_plan(blocks, nwg, slots, tiles, kSplitTiles, (double)nb * (double)nb * (narrow ? 8 : 4) / 5e6, run, narrow);
 }
 
 size_t moment_fp8_ws(int64_t nb, int64_t blocks, int64_t tiles) {

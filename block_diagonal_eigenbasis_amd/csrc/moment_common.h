@@ -38,15 +38,16 @@ hipError_t launch_moment_reduce(const MomentArgs &a, const MomentTable &t, int64
 
 // The plan that run(workgroups, units), an estimate in us, makes fastest for blocks of nwg workgroups each: all blocks
 // whole, those of whole rounds over the chip's slots whole and the rest split along their units of tokens, or all of
-// them split; at most `most` units in one go, `partial` us for a split's sums, and 5 us for the launch that adds them up.
+// them split (`some` false: all or none); at most `most` units in one go, `partial` us for a split's sums, and 5 us for the launch that adds them up.
 template <class Run>
-MomentPlan moment_plan(int64_t blocks, int64_t nwg, int64_t slots, int64_t units, int64_t most, double partial, Run run) {
+MomentPlan moment_plan(int64_t blocks, int64_t nwg, int64_t slots, int64_t units, int64_t most, double partial, Run run,
+                       bool some = true) {
     const int64_t least = (units + most - 1) / most;
     MomentPlan best{0, 1};
     double cost = 1e300;
     const int64_t full = blocks * nwg / slots * slots / nwg;
     for (const int64_t whole : {blocks, full, (int64_t)0}) {
-        if (whole > 0 && least > 1) continue;
+        if (whole > 0 && (least > 1 || (!some && whole < blocks))) continue;
         const int64_t rest = blocks - whole;
         for (int64_t ns = least; ns <= units && ns <= least + 63; ++ns) {
             const int64_t per = (units + ns - 1) / ns;
