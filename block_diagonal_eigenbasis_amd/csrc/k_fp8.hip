@@ -7,6 +7,10 @@
 // 2 KB; the paddings below make every LDS access of a wave fall in distinct banks.  HBM bounds it.
 // The conversions are gfx950's scaled ones (v_cvt_scalef32_pk_fp8_f32 and .._bf8_f32): nearest, ties to
 // even.  The scale is chosen so that nothing saturates.
+// Both operands of 16384 x 1600 in bf16 take 25 us (4.2 TB/s), of 16384 x 6400 82 (5.1), one operand 17 and 57; with a
+// layer norm on the way 28 and 97: with mean, rstd and the weights a thread needs 134 registers, so that three workgroups
+// share a CU and not four (four: 5 registers spilled, 1 us more).  Each row is read once more than by a kernel
+// that held whole rows, which would have to hold 128 of them.
 #include "layers_common.h"
 
 namespace dobb {
@@ -51,7 +55,7 @@ struct Operands {
 };
 
 template <bool BF16, int FMT, bool SQUARE, bool NORM>
-__global__ void __launch_bounds__(256) k_fp8_quantize(int64_t N, int64_t n, int64_t ldx, unsigned colblocks, const void *X,
+__global__ void __launch_bounds__(256, NORM ? 3 : 4) k_fp8_quantize(int64_t N, int64_t n, int64_t ldx, unsigned colblocks, const void *X,
                                                       NormArgs norm, Operands o) {
     __shared__ __align__(16) uint8_t rl[8 * kRowPitch], cl[8 * kColPitch];
     __shared__ uint32_t top[4][128];
@@ -60,30 +64,53 @@ __global__ void __launch_bounds__(256) k_fp8_quantize(int64_t N, int64_t n, int6
     const int64_t tr = blockIdx.x / colblocks, tc = blockIdx.x % colblocks;
     const int64_t r0 = tr * 128 + 8 * ty, c0 = tc * 128 + 8 * tx;
     constexpr int ES = BF16 ? 2 : 4;
+    [[maybe_unused]] __shared__ float2 stat[NORM ? 128 : 1];
+    [[maybe_unused]] float2 own;
+    if constexpr (NORM)                         // a row's statistics, asked for before X
+        if (tid < 128) {
+            const int64_t r = tr * 128 + tid < N ? tr * 128 + tid : N - 1;
+            own = float2{norm.mean[r], norm.rstd[r]};
+        }
     Raw8<BF16> raw[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {               // rows past the last repeat it; zeros below
         const int64_t r = r0 + i < N ? r0 + i : N - 1;
         raw[i] = load8<BF16>((const char *)X + r * ldx * ES, c0, n);
     }
+    if constexpr (NORM) {
+        if (tid < 128) stat[tid] = own;
+        __syncthreads();
+    }
     float v[8][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) unpack8<BF16>(raw[i], v[i]);
+    for (int i = 0; i < 8; ++i)
+        if (!NORM) unpack8<BF16>(raw[i], v[i]);
     if constexpr (NORM) {
         float w[8], b[8];
         affine8(norm.w, c0, n, norm.w_bf16, 1.f, w);
         affine8(norm.b, c0, n, norm.w_bf16, 0.f, b);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int64_t r = r0 + i < N ? r0 + i : N - 1;
-            const float mean = norm.mean[r], rstd = norm.rstd[r];
+            __builtin_amdgcn_sched_barrier(0);   // (a row at a time: 161 registers without)
+            unpack8<BF16>(raw[i], v[i]);
+            const float mean = stat[8 * ty + i].x, rstd = stat[8 * ty + i].y;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float y = norm_value(v[i][j], mean, rstd, w[j], b[j]);
-                if (BF16) y = bf16_to_f32(f32_to_bf16(y));
-                v[i][j] = c0 + j < n ? y : 0.f;
+            for (int j = 0; j < 8; j += 2) {
+                v[i][j] = norm_value(v[i][j], mean, rstd, w[j], b[j]);
+                v[i][j + 1] = norm_value(v[i][j + 1], mean, rstd, w[j + 1], b[j + 1]);
+                if (BF16) {
+                    const uint32_t y = pack_bf16(v[i][j], v[i][j + 1]);
+                    v[i][j] = __uint_as_float(y << 16);
+                    v[i][j + 1] = __uint_as_float(y & 0xffff0000u);
+                }
             }
         }
+        if (tc * 128 + 128 > n)                  // a tile that ends past the last column: zeros there
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c0 + j >= n)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i][j] = 0.f;
     }
     if (r0 + 8 > N)
 #pragma unroll
