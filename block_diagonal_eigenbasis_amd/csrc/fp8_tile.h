@@ -1,4 +1,4 @@
-// One tile of a product of two FP8 operands (layout: dobb_layers.h) on the matrix cores (not installed).
+// One tile of a product of two FP8 operands (layout: dobb_layers.h) on the matrix cores.
 //
 // Two ways to multiply, by what the result is worth:
 // * v_mfma_scale_f32_32x32x64_f8f6f4 on the codes, with the operands' own scale bytes.  The instruction adds its 64
@@ -21,8 +21,6 @@
 #include "moment_common.h"
 
 namespace dobb {
-
-
 
 typedef __attribute__((address_space(3))) void *lds_void;
 
@@ -86,8 +84,7 @@ struct Fp8Tile {
     uint32_t pairs = ~0u;
     bool same = false;                // the sides are the same rows: B's are not loaded again
 
-    // Rows are read from a multiple of four (scales come by fours): a side's row0 may be any where the tile
-    // leaves room, `fr` then being the place of a wave's rows in the slot.
+    // Codes are read from row0, scales, which come by fours, from the word that holds row0's.
     __device__ __forceinline__ Fp8Tile(const Fp8Side &a_, const Fp8Side &b_) : a(a_), b(b_) {
         const int lane = threadIdx.x & 63;
         part = wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

@@ -1,4 +1,13 @@
-// out = A B^T (+ bias) (+ out) for two FP8 operands (dobb_layers.h).
+// out_ij = sum_t 2^(ea_it + eb_jt) sum_k a_itk b_jtk (+ bias_j) (+ out_ij) for two FP8 operands (dobb_layers.h), t over
+// tiles of 128 entries: the scaled matrix instructions take the exponents with the codes, so nothing is left for the
+// vector units but the epilogue.  Their sums drop what is 2^-13 below the largest of eight products (1.4e-5 of a result
+// of normal data), a hundredth of what rounding to bf16 costs; results in fp32 take codes converted to bf16 (exactly) and
+// that type's instruction, which drops nothing, at half the rate.  Sums are fp32, parts of k are added in their order.
+//
+// Three kernels (matmul_plan): up to 32 rows on one side stream the other operand (HBM bounds it: 11008 x 4096 of 45 MB
+// in 9.4 us); tiles of 64 x 64 or 128 x 128, over parts of k where there are few of them; persistent 256 x 256 tiles.
+// Large products are bound by the matrix cores' power: the scaled instruction alone runs 3.67 PFLOP/s on random
+// codes (4.95 on zeros), the bf16 one 1.67 (2.46).  8192^3: 2.85 PFLOP/s to bf16, 1.52 to fp32.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
