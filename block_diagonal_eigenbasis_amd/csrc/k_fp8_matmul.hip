@@ -13,6 +13,7 @@
 #include <type_traits>
 
 #include "fp8_tile.h"
+#include "load_stream.h"
 
 namespace dobb {
 namespace {
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(256) k_fp8_matmul_thin(Fp8Side a, Fp8Side b, i
 // that it has left is loaded again behind the barrier, three halves ahead, and a tile's results leave while the
 // next one's first slots are on their way.  The loads into LDS are written in assembly (they have no register to
 // return to): the compiler would wait for all of them before each read of LDS.
-constexpr int kBig = 256, kRing = 4;
+constexpr int kBig = 256;
 constexpr int kBigPieces = 2 * kBig * 64, kBigSlot = kBigPieces + 2 * kBig;
 
 __device__ __forceinline__ void dma16(const i32x4 &rsrc, uint32_t lds, uint32_t off) {
@@ -402,7 +403,7 @@ __global__ void __launch_bounds__(256, 1) k_fp8_matmul_big(BigArgs g) {
 #pragma unroll
         for (int part = 0; part < 4; ++part) issue(part, !(k & 1) && part == 0);
     }
-    wait_all_but<25>();
+    wait_all_but<kStartLeft>();
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         read(f0, k, 0);
@@ -415,26 +416,23 @@ __global__ void __launch_bounds__(256, 1) k_fp8_matmul_big(BigArgs g) {
             convert(0, k, 1, f0[k][1], e0[k]);
         }
     int s = 0;                                   // slot of the half that is multiplied
-    // Three slots of the next tile are on their way when a tile's results leave: the waits for them leave out the
-    // stores behind them (32 in bf16, 46 of the 64 in fp32, 63 being the most that a wait can leave).
-    int stored = 0;
-    constexpr int kLeft = EXACT ? 63 : 17 + 32;
+    // Three halves of the next tile are on their way when a tile's results leave: the waits for them, and no others, leave
+    // out the stores behind them (load_stream.h: 32 in bf16, 46 of the 64 in fp32).
+    StreamWaits waits;
+    constexpr int kLeft = stream_left(EXACT);
     for (uint32_t tile = first; tile < tiles; tile += stride) {
         auto pair = [&](auto fresh) DOBB_INLINE {
             step_tile();                         // (a branch behind the products would let the compiler move them past it)
-            wait_all_but<17, kLeft>(stored);
+            wait_all_but<kBehind, kLeft>(waits.next());
             body(fresh, f0, e0, f1, e1, No(), (s + 1) & 3);
-            wait_all_but<17, kLeft>(stored);
+            wait_all_but<kBehind, kLeft>(waits.next());
             body(No(), f1, e0, f0, e1, Yes(), (s + 2) & 3);
 #pragma unroll
             for (int k = 0; k < 8; ++k) e0[k] = e1[k];
             s = (s + 2) & 3;
         };
         pair(Yes());
-        for (int h = 2; h < H; h += 2) {
-            pair(No());
-            stored = 0;
-        }
+        for (int h = 2; h < H; h += 2) pair(No());
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -446,7 +444,8 @@ __global__ void __launch_bounds__(256, 1) k_fp8_matmul_big(BigArgs g) {
             // by 32 rows of 128 bytes: registers to LDS as they lie, LDS to memory in rows, 16 bytes a lane
             constexpr int JS = EXACT ? 1 : 2, ES = EXACT ? 4 : 2;   // fragments side by side, bytes of an entry
             const bool whole = (t.m + 1) * kBig <= g.a.rows && (t.n + 1) * kBig <= g.b.rows;
-            stored = whole && !g.e.accumulate;
+            const bool stored = whole && !g.e.accumulate;
+            waits.stored(stored);
             uint8_t *mine = patch[wave];
             uint8_t *put = mine + col * kPatchRow + (EXACT ? 16 : 8) * half;
             const uint8_t *get = mine + (lane >> 3) * kPatchRow + (lane & 7) * 16;
@@ -517,7 +516,7 @@ __global__ void __launch_bounds__(256, 1) k_fp8_matmul_big(BigArgs g) {
                 }
             }
         } else {
-            stored = 0;
+            waits.stored(false);
             float *mine = (float *)patch[wave];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
