@@ -190,11 +190,17 @@ __global__ void __launch_bounds__(256) k_fp8_matmul_thin(Fp8Side a, Fp8Side b, i
 constexpr int kBig = 256;
 constexpr int kBigPieces = 2 * kBig * 64, kBigSlot = kBigPieces + 2 * kBig;
 
+// m0, which takes the LDS address, is put back: it cannot be named as overwritten, and the compiler may hold a value of
+// its own there.  (The two scalar moves cost nothing that can be measured.)
 __device__ __forceinline__ void dma16(const i32x4 &rsrc, uint32_t lds, uint32_t off) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(rsrc));
+    uint32_t held;
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
+                 : "=&s"(held) : "s"(lds), "v"(off), "s"(rsrc));
 }
 __device__ __forceinline__ void dma4(const i32x4 &rsrc, uint32_t lds, uint32_t off) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(rsrc));
+    uint32_t held;
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dword %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
+                 : "=&s"(held) : "s"(lds), "v"(off), "s"(rsrc));
 }
 __device__ __forceinline__ i32x4 buffer_of(const uint8_t *p, uint32_t bytes) {
     const uint64_t a = (uint64_t)(uintptr_t)p;
