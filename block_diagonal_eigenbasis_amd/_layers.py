@@ -210,7 +210,8 @@ class Fp8Capture:
     micro-batches it holds, each from a tile of 128 tokens of its own (default: one, of operand.K tokens)."""
 
     def __init__(self, operand: Fp8Operand, parts=None):
-        self.operand = operand = Fp8Operand(*operand)
+        operand = Fp8Operand(*operand)
+        self.operand = operand = operand._replace(K=int(operand.K))
         self.parts = (int(operand.K),) if parts is None else tuple(int(k) for k in parts)
         c, s = operand.codes, operand.scales
         T, n = (c.shape[0], c.shape[2]) if c.dim() == 4 else (0, 0)
@@ -224,6 +225,8 @@ class Fp8Capture:
             raise ValueError('the format must be "e4m3" or "e5m2"')
         if not self.parts or any(k < 1 for k in self.parts) or sum(fp8_tiles(k) for k in self.parts) != T:
             raise ValueError("the tiles of the parts do not add up to those of the codes")
+        if fp8_tiles(operand.K) != T:
+            raise ValueError(f"K must be a number of entries that {T} tiles hold, the padding between parts counted; got {operand.K}")
 
     @classmethod
     def quantize(cls, x: torch.Tensor, fmt: str = "e4m3") -> "Fp8Capture":
