@@ -47,6 +47,24 @@ class Fp8Operand(NamedTuple):
     def tiles(self) -> int:
         return self.codes.shape[0]
 
+    @property
+    def tokens(self) -> int:
+        """Entries of a row that are no padding: K, but for the operand of a capture of several micro-batches."""
+        return self.K
+
+
+class _JoinedOperand(Fp8Operand):
+    """The operand of a capture whose K counts the padding of every micro-batch but the last."""
+
+    @property
+    def tokens(self) -> int:
+        return self._tokens
+
+    def _replace(self, **kw):
+        new = super()._replace(**kw)
+        new._tokens = self._tokens
+        return new
+
 
 class _CFp8Operand(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64), ("k", ctypes.c_int64),
@@ -199,8 +217,10 @@ def dobb_accumulate_moment_fp8_grouped(ops, As, nbs, N: int, beta: float = 0.0, 
 
 def dobb_accumulate_moment_fp8(op: Fp8Operand, A: torch.Tensor, nb: int, N: int | None = None, beta: float = 0.0,
                                ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """dobb_accumulate_moment from a capture held as an FP8 operand along its columns, of N tokens (default: op.K)."""
-    _check(_of(_host().moment_fp8, stream, op, (op,), (A,), (nb,), op.K if N is None else N, beta, ws), "dobb_accumulate_moment_fp8")
+    """dobb_accumulate_moment from a capture held as an FP8 operand along its columns, of N tokens (default: op.tokens, that
+    is op.K; for the operand of an Fp8Capture of several micro-batches their tokens, without the padding between
+    them)."""
+    _check(_of(_host().moment_fp8, stream, op, (op,), (A,), (nb,), op.tokens if N is None else N, beta, ws), "dobb_accumulate_moment_fp8")
     return A
 
 
@@ -227,6 +247,9 @@ class Fp8Capture:
             raise ValueError("the tiles of the parts do not add up to those of the codes")
         if fp8_tiles(operand.K) != T:
             raise ValueError(f"K must be a number of entries that {T} tiles hold, the padding between parts counted; got {operand.K}")
+        if sum(self.parts) != operand.K:
+            self.operand = _JoinedOperand(*operand)
+            self.operand._tokens = sum(self.parts)
 
     @classmethod
     def quantize(cls, x: torch.Tensor, fmt: str = "e4m3") -> "Fp8Capture":
