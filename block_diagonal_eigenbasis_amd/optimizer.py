@@ -319,15 +319,9 @@ class DobbGroup:
             need = part.need(self, N) if N > self.n_tokens else 0
             mx4 = [i for i in part.idx if isinstance(xs[i], Mx4Capture)]
             fp8 = [i for i in part.idx if isinstance(xs[i], Fp8Capture)]
-            for i in mx4 + fp8:
-                if xs[i].shape[1] != self.cap_dim(i) or xs[i].device != self.device:
-                    raise ValueError(f"capture {i} must hold (tokens x {self.cap_dim(i)}) on {self.device}")
             dense = [i for i in part.idx if not isinstance(xs[i], (Mx4Capture, Fp8Capture))] if mx4 or fp8 else part.idx
-            for i in dense:
-                x = xs[i]
-                if x.dim() != 2 or x.shape[1] != self.cap_dim(i) or not x.is_contiguous() or x.device != self.device:
-                    raise ValueError(f"capture {i} must be a contiguous (tokens x {self.cap_dim(i)}) tensor")
-                _abi._dtype_code(x)
+            for i in part.idx:
+                self._check_capture(i, xs[i])
             mx4 = _split(mx4, lambda i: (xs[i].tiles, xs[i].shape[0]))
             fp8 = _split(fp8, lambda i: (xs[i].tiles, xs[i].shape[0], xs[i].operand.fmt))
             dense = _split(dense, lambda i: (xs[i].dtype, xs[i].shape[0]))
@@ -339,6 +333,16 @@ class DobbGroup:
                 need = max(need, _abi.dobb_workspace_size(_abi.DOBB_OP_ACCUMULATE, self._cap_shapes(sub), xs[sub[0]].shape[0]))
             plans[part] = _Plan(mx4, fp8, dense, need)
         return plans
+
+    def _check_capture(self, i: int, x) -> None:
+        """Refuse a capture that the calls for weight i would not take."""
+        if isinstance(x, (Mx4Capture, Fp8Capture)):
+            if x.shape[1] != self.cap_dim(i) or x.device != self.device:
+                raise ValueError(f"capture {i} must hold (tokens x {self.cap_dim(i)}) on {self.device}")
+            return
+        if x.dim() != 2 or x.shape[1] != self.cap_dim(i) or not x.is_contiguous() or x.device != self.device:
+            raise ValueError(f"capture {i} must be a contiguous (tokens x {self.cap_dim(i)}) tensor")
+        _abi._dtype_code(x)
 
     def _cap_shapes(self, sub):
         return [(1, self.cap_dim(i), self.nb[i]) for i in sub]
@@ -469,6 +473,10 @@ class DobbGroup:
         return graph
 
 
+def _held_as(x) -> str:
+    return f"{type(x).__name__} in {x.operand.fmt}" if isinstance(x, Fp8Capture) else type(x).__name__
+
+
 class Dobb(torch.optim.Optimizer):
     """torch.optim interface: 2-D parameters only, each with a block size (default: n // blocks).
 
@@ -515,6 +523,7 @@ class Dobb(torch.optim.Optimizer):
         axis = 1 if self.side == "input" else 0
         nbs = [block_size or p.shape[axis] // blocks for p in params]
         self._params = params
+        self._index = {id(p): i for i, p in enumerate(params)}
         self._group = DobbGroup([p.data for p in params], nbs, lr=lr, weight_decay=weight_decay,
                                 momentum=momentum, tau=tau, nesterov=nesterov, streams=streams,
                                 basis_dtype=basis_dtype, side=self.side)
@@ -541,7 +550,9 @@ class Dobb(torch.optim.Optimizer):
         """Record (tokens x n) input activations of `param` (Dobb), or (tokens x m) output gradients
         (Dobb-G), for the next refresh: the first call per refresh iteration, or every call with
         capture="all".  A call without tokens is passed over.  x is a tensor, or a capture that is held already (an
-        ``Mx4Capture`` or ``Fp8Capture``: kept as it is, not copied, with capture="all" for every micro-batch)."""
+        ``Mx4Capture`` or ``Fp8Capture``: kept as it is, not copied, with capture="all" for every micro-batch).  What a
+        step could not take is refused here: another width, device or type, or another format than the weight's captures
+        before."""
         held = isinstance(x, (Mx4Capture, Fp8Capture))
         if not held:
             x = x.detach().reshape(-1, x.shape[-1])
@@ -550,10 +561,12 @@ class Dobb(torch.optim.Optimizer):
         if not held:
             x = (Mx4Capture.quantize(x) if self.capture_format == "mx4" else
                  Fp8Capture.quantize(x) if self.capture_format == "fp8" else x.contiguous())
-        before = self._captured.setdefault(id(param), [])
-        if before and type(before[0]) is not type(x):
-            raise ValueError(f"captures of one weight must be held alike: {type(before[0]).__name__} before, now {type(x).__name__}")
-        before.append(x)
+        if id(param) in self._index:
+            self._group._check_capture(self._index[id(param)], x)
+        before = self._captured.get(id(param), [])
+        if before and _held_as(before[0]) != _held_as(x):
+            raise ValueError(f"captures of one weight must be held alike: {_held_as(before[0])} before, now {_held_as(x)}")
+        self._captured[id(param)] = before + [x]
 
     def attach_capture_hooks(self, modules):
         """Hooks on nn.Linear modules whose weights this optimizer owns: on refresh iterations their

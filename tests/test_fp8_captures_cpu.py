@@ -9,6 +9,7 @@ import torch
 
 import block_diagonal_eigenbasis_amd as dobb
 from block_diagonal_eigenbasis_amd import _layers
+from block_diagonal_eigenbasis_amd.optimizer import Dobb, Mx4Capture
 
 
 def operand(T, n, K, fmt="e4m3"):
@@ -50,3 +51,48 @@ def test_the_default_divisor_of_joined_captures_is_their_tokens(monkeypatch):
                         (dobb.Fp8Capture(operand(2, 6, 256), (100, 77)).operand, None, 177)):
         assert dobb.dobb_accumulate_moment_fp8(op, A, 3, N) is A
         assert seen.pop() == want
+
+
+def _held(kind, N=50, n=6):
+    if kind == "mx4":
+        T = dobb.mx4_tiles(N)
+        return Mx4Capture(torch.zeros(T, 4, n, 16, dtype=torch.uint8), torch.zeros(T, n, 4, dtype=torch.uint8), (N,))
+    return torch.zeros(N, n) if kind == "native" else dobb.Fp8Capture(operand(dobb.fp8_tiles(N), n, N, kind))
+
+
+@pytest.mark.parametrize("first,second", [("e4m3", "e5m2"), ("e5m2", "e4m3"), ("e4m3", "mx4"), ("native", "e4m3"), ("mx4", "native")])
+def test_captures_that_cannot_be_joined_are_refused_when_they_come(first, second):
+    """.. and not by every step from then on."""
+    p = torch.nn.Parameter(torch.zeros(8, 6))
+    opt = Dobb([p], block_size=3, capture="all")
+    opt.capture(p, _held(first))
+    with pytest.raises(ValueError, match="held alike"):
+        opt.capture(p, _held(second))
+    opt.capture(p, _held(first, 7))
+    assert [c.shape[0] for c in opt._captured[id(p)]] == [50, 7]
+
+
+@pytest.mark.parametrize("policy", ["first", "all"])
+@pytest.mark.parametrize("kind", ["native", "e4m3", "e5m2", "mx4"])
+@pytest.mark.parametrize("basis", ["activation", "output_gradient"])
+def test_a_capture_of_another_width_is_refused_when_it_comes(policy, kind, basis):
+    p = torch.nn.Parameter(torch.zeros(9, 6))
+    opt = Dobb([p], block_size=3, capture=policy, basis=basis)
+    for n in (3, 6, 9):
+        if n != (6 if basis == "activation" else 9):
+            with pytest.raises(ValueError, match="capture 0"):
+                opt.capture(p, _held(kind, n=n))
+    assert not opt._captured
+    opt.capture(p, _held(kind, n=6 if basis == "activation" else 9))
+    assert len(opt._captured) == 1
+
+
+def test_a_capture_of_another_type_is_refused_when_it_comes():
+    p = torch.nn.Parameter(torch.zeros(8, 6))
+    opt = Dobb([p], block_size=3)
+    with pytest.raises(TypeError):
+        opt.capture(p, torch.zeros(5, 6).half())
+    assert not opt._captured
+    with pytest.raises(ValueError):
+        opt.capture(p, torch.zeros(5, 6, device="meta"))
+    assert not opt._captured
