@@ -263,7 +263,7 @@ class Fp8Capture:
     def cat(cls, captures) -> "Fp8Capture":
         """Captures of several micro-batches as one."""
         captures = list(captures)
-        if len(captures) == 1:
+        if len(captures) == 1 and captures[0].aligned:
             return captures[0]
         if not captures or len({(c.shape[1], c.operand.fmt) for c in captures}) != 1:
             raise ValueError("captures of one width and format, at least one")
@@ -288,6 +288,11 @@ class Fp8Capture:
             dobb_fp8_dequantize(op, dtype, transpose=True, out=out[row:row + k])
             tile, row = tile + t, row + k
         return out
+
+    @property
+    def aligned(self) -> bool:
+        """Whether the calls take the tensors as they lie (a copy, `cat`'s too, always is)."""
+        return self.operand.codes.data_ptr() % 16 == 0 and self.operand.scales.data_ptr() % 4 == 0
 
     @property
     def shape(self):

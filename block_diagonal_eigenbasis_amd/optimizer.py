@@ -64,7 +64,7 @@ class Mx4Capture:
     def cat(cls, captures) -> "Mx4Capture":
         """Captures of several micro-batches as one."""
         captures = list(captures)
-        if len(captures) == 1:
+        if len(captures) == 1 and captures[0].aligned:
             return captures[0]
         if not captures or len({c.shape[1] for c in captures}) != 1:
             raise ValueError("captures of one width, at least one")
@@ -87,6 +87,11 @@ class Mx4Capture:
             _ops.dobb_mx4_dequantize(self.codes[tile:tile + t], self.scales[tile:tile + t], k, dtype, out=out[row:row + k])
             tile, row = tile + t, row + k
         return out
+
+    @property
+    def aligned(self) -> bool:
+        """Whether the moment takes the tensors as they lie (a copy, `cat`'s too, always is)."""
+        return self.codes.data_ptr() % 16 == 0 and self.scales.data_ptr() % 4 == 0
 
     @property
     def shape(self):
@@ -339,6 +344,8 @@ class DobbGroup:
         if isinstance(x, (Mx4Capture, Fp8Capture)):
             if x.shape[1] != self.cap_dim(i) or x.device != self.device:
                 raise ValueError(f"capture {i} must hold (tokens x {self.cap_dim(i)}) on {self.device}")
+            if not x.aligned:
+                raise ValueError(f"capture {i}: codes must be aligned to 16 bytes and scales to 4")
             return
         if x.dim() != 2 or x.shape[1] != self.cap_dim(i) or not x.is_contiguous() or x.device != self.device:
             raise ValueError(f"capture {i} must be a contiguous (tokens x {self.cap_dim(i)}) tensor")
@@ -550,9 +557,9 @@ class Dobb(torch.optim.Optimizer):
         """Record (tokens x n) input activations of `param` (Dobb), or (tokens x m) output gradients
         (Dobb-G), for the next refresh: the first call per refresh iteration, or every call with
         capture="all".  A call without tokens is passed over.  x is a tensor, or a capture that is held already (an
-        ``Mx4Capture`` or ``Fp8Capture``: kept as it is, not copied, with capture="all" for every micro-batch).  What a
-        step could not take is refused here: another width, device or type, or another format than the weight's captures
-        before."""
+        ``Mx4Capture`` or ``Fp8Capture``: kept as it is, copied only if it is not aligned, with capture="all" for every
+        micro-batch).  What a step could not take is refused here: another width, device or type, or another format
+        than the weight's captures before."""
         held = isinstance(x, (Mx4Capture, Fp8Capture))
         if not held:
             x = x.detach().reshape(-1, x.shape[-1])
@@ -561,6 +568,8 @@ class Dobb(torch.optim.Optimizer):
         if not held:
             x = (Mx4Capture.quantize(x) if self.capture_format == "mx4" else
                  Fp8Capture.quantize(x) if self.capture_format == "fp8" else x.contiguous())
+        if held and not x.aligned:
+            x = type(x).cat([x])
         if id(param) in self._index:
             self._group._check_capture(self._index[id(param)], x)
         before = self._captured.get(id(param), [])

@@ -9,7 +9,7 @@ import torch
 
 import block_diagonal_eigenbasis_amd as dobb
 from block_diagonal_eigenbasis_amd import _layers
-from block_diagonal_eigenbasis_amd.optimizer import Dobb, Mx4Capture
+from block_diagonal_eigenbasis_amd.optimizer import Dobb, DobbGroup, Mx4Capture
 
 
 def operand(T, n, K, fmt="e4m3"):
@@ -96,3 +96,32 @@ def test_a_capture_of_another_type_is_refused_when_it_comes():
     with pytest.raises(ValueError):
         opt.capture(p, torch.zeros(5, 6, device="meta"))
     assert not opt._captured
+
+
+def _shifted(t):
+    """t at an address that is not a multiple of 4."""
+    raw = torch.zeros(t.numel() + 16, dtype=torch.uint8)
+    out = raw[(1 - raw.data_ptr()) % 4:][:t.numel()].view(t.shape)
+    out.copy_(t)
+    return out
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "mx4"])
+def test_a_capture_that_is_not_aligned_is_refused_before_anything_is_enqueued(kind):
+    """The C call refuses it, but only after the calls for other weights."""
+    c = _held(kind, 200)
+    for part in ("codes", "scales"):
+        if kind == "mx4":
+            odd = Mx4Capture(*(_shifted(t) if k == part else t for k, t in (("codes", c.codes), ("scales", c.scales))), c.parts)
+        else:
+            odd = dobb.Fp8Capture(c.operand._replace(**{part: _shifted(getattr(c.operand, part))}))
+        g = DobbGroup([torch.zeros(8, 6)], [3])
+        with pytest.raises(ValueError, match="aligned"):
+            g._plan([odd])
+        g._plan([type(odd).cat([odd])])
+        p = torch.nn.Parameter(torch.zeros(8, 6))
+        opt = Dobb([p], block_size=3)
+        opt.capture(p, odd)                                       # copied, not kept as it is
+        (got,) = opt._captured[id(p)]
+        assert got.aligned and not odd.aligned and got.parts == odd.parts and got.shape == odd.shape
+        g._plan([got])
