@@ -627,7 +627,7 @@ hipError_t launch_fp8_matmul(const dobb_fp8_operand &A, const dobb_fp8_operand &
         if (tm * tn >= 0x7fffffff - 256 || 2 * T > 0x7ffffff0) return hipErrorInvalidValue;
         const BigArgs g{a, b, (uint32_t)tm, (uint32_t)tn, (int)(2 * T), e};
         const dim3 grid((unsigned)std::min<int64_t>(tm * tn, 256));
-#define DOBB_FP8_BIG(F, G, EX) DOBB_LAUNCH("fp8_matmul", s, (k_fp8_matmul_big<F, G, EX>), grid, dim3(256), 0, g)
+#define DOBB_FP8_BIG(F, G, EX) DOBB_LAUNCH("fp8_matmul_large", s, (k_fp8_matmul_big<F, G, EX>), grid, dim3(256), 0, g)
         DOBB_FP8_BY(DOBB_FP8_BIG);
 #undef DOBB_FP8_BIG
         return hipGetLastError();
