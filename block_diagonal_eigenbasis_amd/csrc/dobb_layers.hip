@@ -71,7 +71,7 @@ dobb_status check_made(int64_t N, int64_t n, const dobb_fp8_operand *rows, const
         if (op->rows != (op == rows ? N : n) || op->k != (op == rows ? n : N)) return DOBB_ERR_SHAPE;
     }
     if (rows && cols && rows->format != cols->format) return DOBB_ERR_DTYPE;
-    return fp8_tiles(N) <= 0x7fffffff / fp8_tiles(n) ? DOBB_OK : DOBB_ERR_SHAPE;
+    return fp8_tiles(N) <= kMaxWorkgroups / fp8_tiles(n) ? DOBB_OK : DOBB_ERR_SHAPE;
 }
 
 size_t grad_ws(int64_t N, int64_t n) { return al256((size_t)norm_grad_groups(N, n) * 2 * (size_t)n * 4); }
@@ -252,7 +252,7 @@ dobb_status dobb_fp8_dequantize(const dobb_fp8_operand *op, int32_t transpose, v
         const int64_t R = transpose ? op->k : op->rows, C = transpose ? op->rows : op->k;
         st = check_matrix(out, R, C, out_dtype, ldo);
         if (st != DOBB_OK) return st;
-        if (fp8_tiles(op->k) > 0x1fffffff / fp8_tiles(op->rows)) return DOBB_ERR_SHAPE;   // workgroups of 32 rows of a tile
+        if (fp8_read_tiles(op->k, transpose) > kMaxWorkgroups / fp8_read_rows(op->rows, transpose)) return DOBB_ERR_SHAPE;
         Spans s;
         s.operand(*op, false);
         s.matrix(out, R, C, out_dtype, ldo, true);

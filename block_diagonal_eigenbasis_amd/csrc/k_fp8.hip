@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(256) k_fp8_dequantize_t(int64_t R, int64_t K, 
 hipError_t launch_fp8_quantize(int64_t N, int64_t n, const void *X, bool bf16, int64_t ldx, bool square, const NormArgs &norm,
                                const dobb_fp8_operand *rows, const dobb_fp8_operand *cols, hipStream_t s) {
     const int64_t tr = fp8_tiles(N), tc = fp8_tiles(n);
-    if (tr > 0x7fffffff / tc) return hipErrorInvalidValue;
+    if (tr > kMaxWorkgroups / tc) return hipErrorInvalidValue;
     const Operands o{rows ? (uint4 *)rows->codes : nullptr, rows ? (uint8_t *)rows->scales : nullptr,
                      cols ? (uint4 *)cols->codes : nullptr, cols ? (uint8_t *)cols->scales : nullptr};
     const bool e5 = (rows ? rows : cols)->format == DOBB_E5M2;
@@ -316,8 +316,8 @@ hipError_t launch_fp8_quantize(int64_t N, int64_t n, const void *X, bool bf16, i
 }
 
 hipError_t launch_fp8_dequantize(const dobb_fp8_operand &op, bool transpose, void *out, bool bf16, int64_t ldo, hipStream_t s) {
-    const int64_t rb = transpose ? (op.rows + 127) / 128 : (op.rows + 31) / 32, T = fp8_tiles(op.k) * (transpose ? 2 : 1);
-    if (T > 0x7fffffff / rb) return hipErrorInvalidValue;
+    const int64_t rb = fp8_read_rows(op.rows, transpose), T = fp8_read_tiles(op.k, transpose);
+    if (T > kMaxWorkgroups / rb) return hipErrorInvalidValue;
     const dim3 grid((unsigned)(T * rb));
 #define DOBB_FP8_READ(K, F)                                                                                            \
     DOBB_LAUNCH("fp8_dequantize", s, (K<F>), grid, dim3(256), 0, op.rows, op.k, (unsigned)rb, (const uint4 *)op.codes,    \

@@ -634,7 +634,7 @@ hipError_t launch_fp8_matmul(const dobb_fp8_operand &A, const dobb_fp8_operand &
     }
     const int64_t size = p.kind == MatmulPlan::kTile64 ? 64 : 128, tn = tiles(B.rows, size), wgs = tiles(A.rows, size) * tn * p.nsplit;
     const int64_t quads = A.rows * ((B.rows + 3) / 4);
-    if (wgs > 0x7fffffff || quads / 256 >= 0x7fffffff) return hipErrorInvalidValue;
+    if (wgs > kMaxWorkgroups || (p.nsplit > 1 && quads / 256 >= kMaxWorkgroups)) return hipErrorInvalidValue;
 #define DOBB_FP8_TILE(F, G, EX)                                                                                                        \
     do {                                                                                                                              \
         if (size == 64) DOBB_LAUNCH("fp8_matmul", s, (k_fp8_matmul<64, 64, 6, F, G, EX>), dim3((unsigned)wgs), dim3(256), 0, a, b, T, (int)tn, p.nsplit, e, ws); \

@@ -188,7 +188,7 @@ hipError_t launch_moment_fp8(const MomentArgs &a, bool e5m2, hipStream_t s) {
     const int nwg = a.nb <= kNarrow ? 1 : tile_pairs(a.nb), F = (int)(a.nb + 31) / 32;
     const int64_t rest = blocks - a.plan.whole;
     const int64_t wgs = (a.plan.whole + rest * a.plan.nsplit) * nwg;
-    if (a.plan.whole < 0 || rest < 0 || wgs > 0x7fffffff || rest * F * (F + 1) / 2 > 0x7fffffff) return hipErrorInvalidValue;
+    if (a.plan.whole < 0 || rest < 0 || wgs > kMaxWorkgroups || rest * F * (F + 1) / 2 > 0x7fffffff) return hipErrorInvalidValue;
     const double scale = (1.0 - (double)a.beta) / (double)a.N;
     const dim3 grid((unsigned)wgs);
 #define DOBB_FP8_NARROW(F, FMT)                                                                                            \

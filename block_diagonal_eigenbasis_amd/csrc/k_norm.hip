@@ -431,7 +431,7 @@ hipError_t launch_layer_norm_backward(const NormGradArgs &a, hipStream_t s) {
     if (shape.ch == 0) {                         // the sums first: dX may be dY itself
         const dim3 grid((unsigned)std::min<int64_t>(a.N, 512));
         const int64_t strips = (n + 2047) / 2048;
-        if (strips > 0x7fffffff / groups) return hipErrorInvalidValue;
+        if (strips > kMaxWorkgroups / groups) return hipErrorInvalidValue;
 #define DOBB_GRAD_STRIPS(D, B) \
     DOBB_LAUNCH("layer_norm_grad_strips", s, (k_norm_grad_strips<D, B>), dim3((unsigned)(strips * groups)), dim3(256), 0, a.N, n, groups, p, part)
         if (part) DOBB_GRAD_T(DOBB_GRAD_STRIPS);

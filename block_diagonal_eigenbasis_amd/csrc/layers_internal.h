@@ -8,6 +8,7 @@ namespace dobb {
 
 constexpr int64_t kFp8Tile = 128;
 inline int64_t fp8_tiles(int64_t k) { return k / kFp8Tile + (k % kFp8Tile != 0); }
+constexpr int64_t kMaxWorkgroups = ((int64_t)1 << 24) - 1;   // of 256 threads: a launch holds fewer than 2^32
 inline int64_t fp8_pitch(int64_t rows) { return (rows + 3) / 4 * 4; }   // bytes of a tile's scales
 
 // What normalises a matrix while it is quantised (mean == nullptr: nothing)
@@ -42,6 +43,9 @@ hipError_t launch_layer_norm_backward(const NormGradArgs &a, hipStream_t s);
 
 hipError_t launch_fp8_quantize(int64_t N, int64_t n, const void *X, bool bf16, int64_t ldx, bool square, const NormArgs &norm,
                                const dobb_fp8_operand *rows, const dobb_fp8_operand *cols, hipStream_t s);
+// workgroups of a read-back: 32 rows of a tile each, or with `transpose` 128 rows of half a tile
+inline int64_t fp8_read_rows(int64_t rows, bool transpose) { return transpose ? (rows + 127) / 128 : (rows + 31) / 32; }
+inline int64_t fp8_read_tiles(int64_t k, bool transpose) { return fp8_tiles(k) * (transpose ? 2 : 1); }
 hipError_t launch_fp8_dequantize(const dobb_fp8_operand &op, bool transpose, void *out, bool bf16, int64_t ldo, hipStream_t s);
 
 size_t fp8_matmul_ws(int64_t M, int64_t N, int64_t k);

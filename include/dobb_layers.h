@@ -80,7 +80,8 @@ dobb_status dobb_fp8_quantize(int64_t N, int64_t n, const void *X, dobb_dtype x_
                               const dobb_fp8_operand *along_rows, const dobb_fp8_operand *along_cols,
                               dobb_stream_t stream);
 /* out: rows x k, or k x rows with `transpose` (fp32 or bf16): the values, exact in fp32 and, from 2^-126 up, in
- * bf16. */
+ * bf16.  DOBB_ERR_SHAPE from 2^36 entries on (whole tiles counted; 2^37 with `transpose`, and 2^38 for dobb_fp8_quantize):
+ * more than a launch holds. */
 dobb_status dobb_fp8_dequantize(const dobb_fp8_operand *op, int32_t transpose, void *out, dobb_dtype out_dtype,
                                 int64_t ldo, dobb_stream_t stream);
 /* dobb_layer_norm with its output as FP8 operands: bit for bit dobb_fp8_quantize of the Y that dobb_layer_norm
