@@ -208,7 +208,7 @@ hipError_t launch_moment_fp8(const MomentArgs &a, bool e5m2, hipStream_t s) {
 #undef DOBB_FP8_MOMENT
 #undef DOBB_FP8_NARROW
     const hipError_t e = hipGetLastError();
-    return e != hipSuccess || rest == 0 ? e : launch_moment_reduce(a, t, blocks, s);
+    return e != hipSuccess || rest == 0 ? e : launch_moment_reduce("moment_fp8_reduce", a, t, blocks, s);
 }
 
 }  // namespace dobb

@@ -381,9 +381,9 @@ MomentPlan moment_mx4_plan(int64_t nb, int64_t blocks, int64_t tiles) {
     return moment_plan(blocks, nwg, slots, tp, kSplitPairs, partial, run);
 }
 
-hipError_t launch_moment_reduce(const MomentArgs &a, const MomentTable &t, int64_t blocks, hipStream_t s) {
+hipError_t launch_moment_reduce(const char *name, const MomentArgs &a, const MomentTable &t, int64_t blocks, hipStream_t s) {
     const int F = (int)(a.nb + 31) / 32, pairs = F * (F + 1) / 2;
-    DOBB_LAUNCH("moment_reduce", s, k_moment_reduce, dim3((unsigned)((blocks - a.plan.whole) * pairs)), dim3(256), 0, a.count, (int)a.nb,
+    DOBB_LAUNCH(name, s, k_moment_reduce, dim3((unsigned)((blocks - a.plan.whole) * pairs)), dim3(256), 0, a.count, (int)a.nb,
                 a.plan.whole, a.plan.nsplit, pairs, (double)a.beta, (1.0 - (double)a.beta) / (double)a.N, a.partial, t);
     return hipGetLastError();
 }
@@ -442,7 +442,7 @@ hipError_t launch_moment_mx4(const MomentArgs &a, hipStream_t s) {
     else e = hipErrorInvalidValue;
     if (e == hipSuccess) e = hipGetLastError();
     if (e != hipSuccess || rest == 0) return e;
-    return launch_moment_reduce(a, t, blocks, s);
+    return launch_moment_reduce("moment_mx4_reduce", a, t, blocks, s);
 }
 
 }  // namespace dobb

@@ -33,8 +33,8 @@ inline MomentTable moment_table(const MomentArgs &a, int64_t *blocks) {
     return t;
 }
 
-// the splits' sums of the blocks that a launch has split (fp64), into A
-hipError_t launch_moment_reduce(const MomentArgs &a, const MomentTable &t, int64_t blocks, hipStream_t s);
+// the splits' sums of the blocks that a launch has split (fp64), into A; `name` is the launch timer's
+hipError_t launch_moment_reduce(const char *name, const MomentArgs &a, const MomentTable &t, int64_t blocks, hipStream_t s);
 
 // The plan that run(workgroups, units), an estimate in us, makes fastest for blocks of nwg workgroups each: all blocks
 // whole, those of whole rounds over the chip's slots whole and the rest split along their units of tokens, or all of
