@@ -618,8 +618,10 @@ class Dobb(torch.optim.Optimizer):
             xs = []
             for p in self._params:
                 parts = self._captured[id(p)]
-                xs.append(type(parts[0]).cat(parts) if isinstance(parts[0], (Mx4Capture, Fp8Capture)) else
-                          parts[0] if len(parts) == 1 else torch.cat(parts, 0))
+                if len(parts) > 1:               # the joined capture takes the place of its parts, weight by weight
+                    held = isinstance(parts[0], (Mx4Capture, Fp8Capture))
+                    self._captured[id(p)] = parts = [type(parts[0]).cat(parts) if held else torch.cat(parts, 0)]
+                xs.append(parts[0])
             if g.refreshes == 0:
                 g.refresh_step(xs, 0.0, _abi.DOBB_REFRESH_EXACT, 0, grads, warm_start=False)
             else:

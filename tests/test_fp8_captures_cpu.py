@@ -2,7 +2,9 @@
 tensors, and captures of one weight agree with each other before a step takes them.
 """
 import copy
+import gc
 import types
+import weakref
 
 import pytest
 import torch
@@ -125,3 +127,29 @@ def test_a_capture_that_is_not_aligned_is_refused_before_anything_is_enqueued(ki
         (got,) = opt._captured[id(p)]
         assert got.aligned and not odd.aligned and got.parts == odd.parts and got.shape == odd.shape
         g._plan([got])
+
+
+@pytest.mark.parametrize("kind", ["native", "e4m3", "mx4"])
+def test_joined_captures_take_the_place_of_their_parts(monkeypatch, kind):
+    """With capture="all" a refresh does not hold every weight's captures twice."""
+    params = [torch.nn.Parameter(torch.zeros(8, 6)) for _ in range(3)]
+    opt = Dobb(params, block_size=3, capture="all")
+    parts = []
+    for N in (50, 7, 130):
+        for p in params:
+            opt.capture(p, _held(kind, N))
+            parts.append(weakref.ref(opt._captured[id(p)][-1]))
+    assert all(r() is not None for r in parts)
+    seen = []
+
+    def refresh_step(xs, *args, **kw):
+        gc.collect()
+        seen.append([x.shape[0] for x in xs])
+        assert all(r() is None for r in parts)
+        if len(seen) == 1:
+            raise RuntimeError("this step fails")
+    monkeypatch.setattr(opt._group, "refresh_step", refresh_step)
+    with pytest.raises(RuntimeError, match="this step fails"):
+        opt.step()
+    opt.step()                                                    # with what was joined
+    assert seen == [[187] * 3] * 2 and not opt._captured
