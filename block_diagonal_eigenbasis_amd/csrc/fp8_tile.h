@@ -12,9 +12,9 @@
 // long as both sides agree).  A workgroup of four waves computes TM x TN entries, a wave a quarter of them.
 // Half a tile of k (64 entries) of both operands is a slot of TM + TN pieces of 64 bytes and their scales,
 // which the memory engine writes straight into LDS; of NS slots one is multiplied while the others are on
-// their way.  The slots are separate LDS arrays and the loop is unrolled over them, so that the compiler waits,
-// before a read, only for the loads into that slot.  Rows past an operand's last and slots past the last
-// are loaded from past the end of the buffer, as zeros.
+// their way.  What orders loads and reads is the wait and barrier at the end of each half: all but the last NS - 2 halves'
+// loads done, on every wave, before the next half is read.
+// Rows past an operand's last and slots past the last are loaded from past the end of the buffer, as zeros.
 #pragma once
 
 #include "layers_common.h"

@@ -5,9 +5,9 @@
 // that type's instruction, which drops nothing, at half the rate.  Sums are fp32, parts of k are added in their order.
 //
 // Three kernels (matmul_plan): up to 32 rows on one side stream the other operand (HBM bounds it: 11008 x 4096 of 45 MB
-// in 9.4 us); tiles of 64 x 64 or 128 x 128, over parts of k where there are few of them; persistent 256 x 256 tiles.
-// Large products are bound by the matrix cores' power: the scaled instruction alone runs 3.67 PFLOP/s on random
-// codes (4.95 on zeros), the bf16 one 1.67 (2.46).  8192^3: 2.85 PFLOP/s to bf16, 1.52 to fp32.
+// in 10.3 us); tiles of 64 x 64 or 128 x 128, over parts of k where there are few of them; persistent 256 x 256 tiles.
+// Large products: the scaled instruction alone runs 3.67 PFLOP/s on random codes (4.95 on zeros: power sets the clock;
+// the 16x16x128 one 4.29), the bf16 one 1.67 (2.46).  8192^3: 2.70 to 2.82 PFLOP/s to bf16, 1.49 to 1.52 to fp32.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

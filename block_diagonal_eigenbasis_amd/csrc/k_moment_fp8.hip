@@ -157,7 +157,8 @@ __global__ void __launch_bounds__(256, 2) k_moment_fp8_wide(int cnt, int nb, int
 // How a launch splits its tokens (moment_plan).  A tile takes a narrow workgroup 0.12 us a fragment (four at once; 1.8 us
 // at 128 columns where all slots read at the memory's rate), a wide one 1.2 us alone on its CU and 2 us beside two others.
 // Wide blocks are split all or none: workgroups of a second round begin as those of the first end, so that no round of
-// whole blocks ends at once (16384 tokens, 192 blocks of 400: none split 707 us, all in two 693, 39 of them in two 771;
+// whole blocks ends at once (16384 tokens, 192 blocks of 400: none split 707 us, all in two 693, 39 of them in two 771; behind
+// another width's launch of the same call none split 672 to 764;
 // 16 blocks: 149 whole, 107 in two, 78 in four, 77 in eight, 89 in sixteen; 32 blocks of 128: 63 whole, 28 in four, 27 in
 // eight, 37 in sixteen).
 MomentPlan moment_fp8_plan(int64_t nb, int64_t blocks, int64_t tiles) {

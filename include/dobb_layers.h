@@ -28,7 +28,8 @@ extern "C" {
  *   mean_t = sum_c x_tc / n,   rstd_t = (sum_c (x_tc - mean_t)^2 / n + eps)^-1/2,
  *   y_tc = (x_tc - mean_t) rstd_t w_c + b_c
  * X, Y, dY, dX: fp32 or bf16, each of its own type, rows of any stride (ld >= n) aligned to their entries
- * only.  weight, bias: fp32 or bf16 [n] (one type), either NULL for ones or zeros.  mean, rstd: fp32 [N].
+ * only.  weight, bias: fp32 or bf16 [n] (one type), either NULL for ones or zeros.  mean, rstd: fp32 [N].  A row whose sum
+ * of entries, or of squares around the mean, passes fp32's largest value has no mean, or an rstd of 0.
  * Statistics and sums over a row are formed in fp32 around the mean, sums over all rows in fp32 over at most
  * 1024 of them and in fp64 across those; results are rounded once to their type.  eps >= 0; with eps = 0 a row of
  * equal entries has an infinite rstd and NaN results.  NaN and infinities stay within their row, and in the
@@ -61,7 +62,7 @@ dobb_status dobb_layer_norm_backward(int64_t N, int64_t n, const void *dY, dobb_
  * block to the format's largest value or below; code = x / 2^e rounded to the nearest value, ties to
  * even (nothing saturates).  A block is 128 entries along k, or with `square` the 128 x 128 entries of
  * a tile, so that the operands along both axes hold the same values.  A block with a NaN or an infinity gets the
- * scale byte 255 and codes 0x7f, and reads back as NaN.  Entries past k of other blocks are zeros.  Operands of several micro-batches
+ * scale byte 255 and codes 0x7f (all 128 x 128 with `square`).  The scale byte 255 is NaN, whatever the codes.  Entries past k of other blocks are zeros.  Operands of several micro-batches
  * along their tokens (k) are joined by laying their tiles one behind the other.
  * -------------------------------------------------------------------------------------------------*/
 typedef enum { DOBB_E4M3 = 0, DOBB_E5M2 = 1 } dobb_fp8_format;
