@@ -7,8 +7,10 @@
 //   fragment pairs on or below the diagonal and hand each other their sums through LDS at the end.
 // k_moment_fp8_wide (128 < nb <= 1024): a workgroup computes 128 x 128 entries on or below the diagonal of a block as
 //   a product of the operand with itself (fp8_tile.h), and leaves out fragment pairs above it or past the block.
-// Rounding: fp32 sums of at most 4096 tokens (narrow, four of those added in fp32) or 16384 (wide) in the
-// accumulators, token splits in fp64 (k_moment_reduce).
+// Rounding: fp32 sums of at most 4096 tokens in the accumulators (four of those added in fp32 by a narrow workgroup), token
+// splits in fp64 (k_moment_reduce).  The matrix instruction cuts what lies below its accumulator's last bits, and a sum of
+// squares only grows: with activations whose tokens differ in size, 16384 tokens in one sum left a block of 400 up to 1.4e-6
+// too small (2-norm), 4096 at most 5.5e-7, where fp32 products of 1024 tokens added in fp64 are 3e-7 off.
 #include <algorithm>
 
 #include "fp8_tile.h"
@@ -17,7 +19,8 @@ namespace dobb {
 namespace {
 
 constexpr int kNarrow = 128;                   // widest block of the narrow kernel
-constexpr int64_t kSplitTiles = 128;           // most tiles of one split: 16384 tokens
+// most tiles of one split, of which a narrow workgroup's waves take a quarter each: 4096 tokens a sum
+constexpr int64_t kNarrowTiles = 128, kWideTiles = 32;
 
 inline __host__ __device__ int tile_pairs(int64_t nb) {
     const int t = (int)((nb + 127) / 128);
@@ -157,10 +160,9 @@ __global__ void __launch_bounds__(256, 2) k_moment_fp8_wide(int cnt, int nb, int
 // How a launch splits its tokens (moment_plan).  A tile takes a narrow workgroup 0.12 us a fragment (four at once; 1.8 us
 // at 128 columns where all slots read at the memory's rate), a wide one 1.2 us alone on its CU and 2 us beside two others.
 // Wide blocks are split all or none: workgroups of a second round begin as those of the first end, so that no round of
-// whole blocks ends at once (16384 tokens, 192 blocks of 400: none split 707 us, all in two 693, 39 of them in two 771; behind
-// another width's launch of the same call none split 672 to 764;
-// 16 blocks: 149 whole, 107 in two, 78 in four, 77 in eight, 89 in sixteen; 32 blocks of 128: 63 whole, 28 in four, 27 in
-// eight, 37 in sixteen).
+// whole blocks ends at once (16384 tokens, 192 blocks of 400: none split 724 us, all in four, as kWideTiles asks for, 750, in
+// eight 820; 16 blocks: 149 whole, 107 in two, 78 in four, 77 in eight, 89 in sixteen; 32 blocks of 128: 63 whole, 28 in four,
+// 27 in eight, 37 in sixteen).
 MomentPlan moment_fp8_plan(int64_t nb, int64_t blocks, int64_t tiles) {
     const bool narrow = nb <= kNarrow;
     const int64_t nwg = narrow ? 1 : tile_pairs(nb), slots = narrow ? (nb <= 96 ? 512 : 256) : 768;
@@ -174,7 +176,7 @@ MomentPlan moment_fp8_plan(int64_t nb, int64_t blocks, int64_t tiles) {
         }
         return t;
     };
-    return moment_plan(blocks, nwg, slots, tiles, kSplitTiles, (double)nb * (double)nb * (narrow ? 8 : 4) / 5e6, run, narrow);
+    return moment_plan(blocks, nwg, slots, tiles, narrow ? kNarrowTiles : kWideTiles, (double)nb * (double)nb * (narrow ? 8 : 4) / 5e6, run, narrow);
 }
 
 size_t moment_fp8_ws(int64_t nb, int64_t blocks, int64_t tiles) {

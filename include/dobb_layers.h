@@ -111,9 +111,9 @@ dobb_status dobb_fp8_matmul(const dobb_fp8_operand *A, const dobb_fp8_operand *B
  * dobb_accumulate_moment from captures held as FP8 operands along the columns (rows = s->n, k tokens):
  *   A_b <- beta * A_b + (1 - beta) * (1/N) * sum_t x_{t,b} x_{t,b}^T   over all ceil(k / 128) tiles.
  * N is the divisor, the tokens the tiles hold (1 <= N <= 128 tiles).  Products are exact (entries below
- * 2^-126 count as zero) and summed in fp32 over at most 16384 tokens, those sums in fp64.  A (symmetric) is read when
- * beta > 0 and the result is exactly symmetric.  beta is a float, and 1 - beta is taken from it exactly.  Grouped:
- * all operands hold the same number of tiles; captures may be shared by several matrices.
+ * 2^-126 count as zero) and summed in fp32 over at most 4096 tokens at a time, four of those sums in fp32 for nb <= 128, the
+ * others in fp64.  A (symmetric) is read when beta > 0 and the result is exactly symmetric.  beta is a float, and 1 - beta
+ * is taken from it exactly.  Grouped: all operands hold the same number of tiles; captures may be shared by several matrices.
  * -------------------------------------------------------------------------------------------------*/
 size_t dobb_moment_fp8_workspace_size(int count, const dobb_shape *shapes, int64_t tiles); /* 0: bad arguments, or no scratch needed */
 dobb_status dobb_accumulate_moment_fp8(const dobb_shape *s, const dobb_fp8_operand *op, int64_t N, float beta, float *A,
