@@ -110,7 +110,7 @@ def _replay(tmp_path, source):
 def test_every_half_is_waited_for(tmp_path):
     r = _replay(tmp_path, REPLAY)
     assert r.returncode == 0, r.stdout
-    assert r.stdout == "3072 cases\n"
+    assert r.stdout == f"{6 * 2 * 4 * 2 * 32} cases\n"
 
 
 @pytest.mark.parametrize("old,new", [("kBehind)", "kBehind + 1)"), ("kStartLeft)", "kStartLeft + 1)"), ("waits.next() ? left", "true ? left"),
